@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe_route.so (include/moe_route.h), with the C names.
+"""ctypes binding of libmoe_route.so (include/moe_route.h, include/moe_layer.h), with the C names.
 
 Argument marshalling only: torch tensors supply device memory and the current HIP stream, and
 every step runs in the library's HIP kernels. If the library is not built, loading fails with an
@@ -21,6 +21,10 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_TOPK = 64
 MOE_NOALLOC_SCRATCH_BYTES = 16 << 20
+MOE_MAX_SEQS = 65536
+MOE_MATMUL_MAX_K = 131056
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+ACT_CODES = {"none": MOE_ACT_NONE, "swiglu": MOE_ACT_SWIGLU}
 
 DTYPE_CODES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3}
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8_e4m3": torch.uint8}
@@ -71,7 +75,15 @@ def load() -> ctypes.CDLL:
         lib.moe_ep_reduce.argtypes = [P, I, I, I, I, I, I, I, P, I, I, P, P, P, P, I, P, P, Z, P]
         lib.moe_ep_combine_reduced.argtypes = [P, I, I, I, I, P, I, P, I, P]
         lib.moe_check_topk.argtypes = [P, I, I, I, P, P]
-        for fn in ("moe_route_topk", "moe_dispatch_layout", "moe_dispatch_pack", "moe_dispatch",
+        F = ctypes.c_float
+        lib.moe_balance_workspace_bytes.argtypes = [I, I, I]
+        lib.moe_balance_workspace_bytes.restype = Z
+        lib.moe_balance_loss.argtypes = [P, P, P, I, I, I, I, F, P, P, P, P, P, Z, P]
+        lib.moe_route_grad.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, F, P, P]
+        lib.moe_quant_rows.argtypes = [P, I, I, I, P, P, P, P]
+        lib.moe_expert_matmul_i8.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, P, I, P]
+        for fn in ("moe_balance_loss", "moe_route_grad", "moe_quant_rows", "moe_expert_matmul_i8",
+                   "moe_route_topk", "moe_dispatch_layout", "moe_dispatch_pack", "moe_dispatch",
                    "moe_route_dispatch", "moe_route_dispatch_noalloc", "moe_combine", "moe_ep_send", "moe_ep_recv",
                    "moe_ep_return", "moe_ep_combine", "moe_ep_partial_rows", "moe_ep_reduce",
                    "moe_ep_combine_reduced", "moe_check_topk"):
@@ -369,4 +381,176 @@ def moe_ep_combine_reduced(partials: torch.Tensor, part_row: torch.Tensor, out: 
     _check("moe_ep_combine_reduced", load().moe_ep_combine_reduced(
         _ptr(partials), _dtype_code(partials), T, H, N, _ptr(part_row), partials.shape[0],
         _ptr(out), _dtype_code(out), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------------------------------------
+# Router training and the experts' product in 8-bit integers (see include/moe_layer.h). These calls
+# check every tensor (device, type, shape, density) before the library sees its pointer, and run
+# on the device of their tensors whichever one is current.
+
+def _arg(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, needs {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t
+
+
+def _matrix(name: str, t: torch.Tensor) -> torch.device:
+    """The device of a call, from its main input."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name}: a 2-d tensor is needed")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, needs a GPU")
+    return t.device
+
+
+def _out(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _arg(name, t, dtype, shape, device)
+
+
+def _enqueue(fn: str, device: torch.device, stream, *args) -> None:
+    """Call a library function on `device`, on `stream` or the device's current stream."""
+    with torch.cuda.device(device):
+        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+
+
+def moe_balance_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
+    return int(load().moe_balance_workspace_bytes(T, E, n_seqs))
+
+
+def alloc_balance_workspace(T: int, E: int, n_seqs: int = 1, device="cuda") -> torch.Tensor:
+    n = max(moe_balance_workspace_bytes(T, E, n_seqs), 1)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float, n_seqs: int = 1,
+                     token_mask: Optional[torch.Tensor] = None,
+                     loss: Optional[torch.Tensor] = None,
+                     expert_counts: Optional[torch.Tensor] = None,
+                     prob_sums: Optional[torch.Tensor] = None,
+                     seq_tokens: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Balance loss of the router; returns (loss [1], expert_counts [S,E], prob_sums [S,E],
+    seq_tokens [S]). token_mask [T] bool or uint8: False marks padding. Without a workspace one
+    is allocated for the call."""
+    dev = _matrix("logits", logits)
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    _arg("logits", logits, torch.float32, (T, E), dev)
+    _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    if token_mask is not None:
+        _arg("token_mask", token_mask, (torch.bool, torch.uint8), (T,), dev)
+    n_seqs = int(n_seqs)
+    if n_seqs < 1 or T % n_seqs:
+        raise ValueError(f"n_seqs: {n_seqs} sequences do not divide {T} tokens")
+    loss = _out("loss", loss, torch.float32, (1,), dev)
+    expert_counts = _out("expert_counts", expert_counts, torch.int32, (n_seqs, E), dev)
+    prob_sums = _out("prob_sums", prob_sums, torch.float32, (n_seqs, E), dev)
+    seq_tokens = _out("seq_tokens", seq_tokens, torch.int32, (n_seqs,), dev)
+    if workspace is None:
+        workspace = alloc_balance_workspace(T, E, n_seqs, dev)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
+        elif stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=dev))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs contiguous memory on {dev}")
+    _enqueue("moe_balance_loss", dev, stream, _ptr(logits), _ptr(topk_idx), _ptr(token_mask), T, E,
+             k, n_seqs, float(alpha), _ptr(loss), _ptr(expert_counts), _ptr(prob_sums),
+             _ptr(seq_tokens), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return loss, expert_counts, prob_sums, seq_tokens
+
+
+def moe_route_grad(logits: torch.Tensor, topk_idx: torch.Tensor,
+                   topk_w: Optional[torch.Tensor] = None, dtopk_w: Optional[torch.Tensor] = None,
+                   token_mask: Optional[torch.Tensor] = None,
+                   expert_counts: Optional[torch.Tensor] = None,
+                   seq_tokens: Optional[torch.Tensor] = None,
+                   dloss: Optional[torch.Tensor] = None, alpha: float = 0.0, n_seqs: int = 1,
+                   dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the router's logits [T,E]: of the balance loss (given expert_counts and
+    seq_tokens), of the routing weights (given topk_w and dtopk_w), or their sum."""
+    dev = _matrix("logits", logits)
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    n_seqs = int(n_seqs)
+    _arg("logits", logits, torch.float32, (T, E), dev)
+    _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    for name, t, dtypes, shape in (
+            ("topk_w", topk_w, torch.float32, (T, k)), ("dtopk_w", dtopk_w, torch.float32, (T, k)),
+            ("token_mask", token_mask, (torch.bool, torch.uint8), (T,)),
+            ("expert_counts", expert_counts, torch.int32, (n_seqs, E)),
+            ("seq_tokens", seq_tokens, torch.int32, (n_seqs,)),
+            ("dloss", dloss, torch.float32, (1,))):
+        if t is not None:
+            _arg(name, t, dtypes, shape, dev)
+    dlogits = _out("dlogits", dlogits, torch.float32, (T, E), dev)
+    _enqueue("moe_route_grad", dev, stream, _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+             _ptr(dtopk_w), _ptr(token_mask), _ptr(expert_counts), _ptr(seq_tokens), _ptr(dloss),
+             T, E, k, n_seqs, float(alpha), _ptr(dlogits))
+    return dlogits
+
+
+def moe_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None, n_rows: Optional[torch.Tensor] = None,
+                   stream=None):
+    """8-bit rows: (q int8 [R,H], scale fp32 [R]) with x about q * scale. n_rows (int32 [1] on
+    the device): only the first n_rows rows are quantised."""
+    dev = _matrix("x", x)
+    R, H = x.shape
+    _arg("x", x, (torch.bfloat16, torch.float32), (R, H), dev)
+    q = _out("q", q, torch.int8, (R, H), dev)
+    scale = _out("scale", scale, torch.float32, (R,), dev)
+    if n_rows is not None:
+        _arg("n_rows", n_rows, torch.int32, (1,), dev)
+    _enqueue("moe_quant_rows", dev, stream, _ptr(x), _dtype_code(x), R, H, _ptr(n_rows), _ptr(q),
+             _ptr(scale))
+    return q, scale
+
+
+def moe_expert_matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
+                         w_scale: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None,
+                         row_token: Optional[torch.Tensor] = None, act: str = "none",
+                         out: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The experts' product of 8-bit rows a [A,K] (scale [A]) with 8-bit weights w [E,N,K] (scale
+    [E,N]; act "swiglu": [E,2N,K], gate channels first); returns out [R,N] in out's type or
+    out_dtype. Row r of expert e (expert_offsets [E+1]) reads row row_token[r] of a, or row r
+    without row_token. Without expert_offsets E must be 1: a plain product."""
+    dev = _matrix("a", a)
+    if act not in ACT_CODES:
+        raise ValueError(f"act: {act!r}, needs one of {sorted(ACT_CODES)}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w: a 3-d tensor is needed")
+    A, K = a.shape
+    E, n_w, _ = w.shape
+    if act == "swiglu" and n_w % 2:
+        raise ValueError(f"w: {n_w} channels do not split into gate and up")
+    N = n_w // 2 if act == "swiglu" else n_w
+    R = A if row_token is None else row_token.numel()
+    _arg("a", a, torch.int8, (A, K), dev)
+    _arg("a_scale", a_scale, torch.float32, (A,), dev)
+    _arg("w", w, torch.int8, (E, n_w, K), dev)
+    _arg("w_scale", w_scale, torch.float32, (E, n_w), dev)
+    if expert_offsets is not None:
+        _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev)
+    if row_token is not None:
+        _arg("row_token", row_token, torch.int32, (R,), dev)
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    _arg("out", out, (torch.bfloat16, torch.float32), (R, N), dev)
+    _enqueue("moe_expert_matmul_i8", dev, stream, _ptr(a), _ptr(a_scale), A, _ptr(row_token),
+             _ptr(w), _ptr(w_scale), _ptr(expert_offsets), R, E, N, K, ACT_CODES[act], _ptr(out),
+             _dtype_code(out))
     return out

@@ -1,0 +1,482 @@
+// moe_experts.hip -- 8-bit rows with a scale for each token, and the experts' product in 8-bit
+// integers (declared in include/moe_layer.h).
+#include "moe_device.h"
+#include "moe_layer.h"
+
+namespace {
+
+using namespace moe_dev;
+
+// ------------------------------------------------------------------------------ 8-bit rows --
+// a = max |x|, q = rint(127 x / a), scale = a / 127. Each row is read once, held in registers
+// between its maximum and its codes, and bound by HBM: 2 (bf16) or 4 (fp32) bytes in and one out
+// for an element. G lanes take a row, with up to NV vectors of 8 elements a lane; longer rows are
+// read a second time, from the cache.
+constexpr int kQuantVec = 8;
+
+template <typename X>
+__device__ __forceinline__ void load8(const X* __restrict__ p, float v[8]);
+
+template <>
+__device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float v[8])
+{
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(x[i] << 16);
+        v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+    }
+}
+
+template <>
+__device__ __forceinline__ void load8(const float* __restrict__ p, float v[8])
+{
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(p);
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The code of x in a row of largest magnitude a, from inv = fl(127 / a) (x and a scaled by a power
+// of two where a is tiny). fl(x inv) lies within 127 * 2^-23 of 127 x / a, so its rounding is right
+// unless it lies that near to a half; there 127 x - r a decides, which fp64 holds exactly: 127 x
+// has 31 bits, r a too, and x >= a / 254 there, so both are multiples of ulp(a) 2^-8 below 2 a.
+__device__ __forceinline__ int32_t code_of(float x, float a, float inv)
+{
+    const float q = x * inv;
+    float r = rintf(q);
+    if (__builtin_fabsf(__builtin_fabsf(q - r) - 0.5f) < 6.0e-5f) {
+        r = floorf(q);                                        // r or r + 1
+        const double d = 2.0 * (127.0 * (double)x - (double)r * (double)a) - (double)a;
+        if (d > 0.0 || (d == 0.0 && ((int32_t)r & 1)))
+            r += 1.0f;
+    }
+    return (int32_t)r;
+}
+
+__device__ __forceinline__ u32x2 codes8(const float v[8], float a, float inv, float up)
+{
+    u32x2 c = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c[i >> 2] |= ((uint32_t)code_of(v[i] * up, a, inv) & 0xFFu) << (8 * (i & 3));
+    return c;
+}
+
+template <typename X, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_quant_rows(const X* __restrict__ x,
+                                                                  int32_t R, int32_t H,
+                                                                  const int32_t* __restrict__ n_rows,
+                                                                  int8_t* __restrict__ q,
+                                                                  float* __restrict__ scale)
+{
+    constexpr int kThreads = G < 256 ? 256 : G;
+    constexpr int kRows = kThreads / G;                       // rows of a workgroup at a time
+    constexpr int kWavesPerRow = G / 64;                      // 0: several rows in a wavefront
+    __shared__ uint32_t s_max[2][kThreads / 64];
+    const int tid = threadIdx.x, g = tid % G;
+    const int32_t rows = n_rows ? min(max(n_rows[0], 0), R) : R;
+    const int nvec = H / kQuantVec;
+    int flip = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+        const int64_t row = r0 + tid / G;
+        const bool live = row < rows;
+        const X* p = x + row * H;
+        float v[NV][kQuantVec];
+        uint32_t m = 0u;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (g + i * G < nvec) {
+                    load8(p + (int64_t)(g + i * G) * kQuantVec, v[i]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kQuantVec; ++c)
+                        v[i][c] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int c = 0; c < kQuantVec; ++c)
+                    m = max(m, abs_bits(v[i][c]));
+            for (int i = g + NV * G; i < nvec; i += G) {
+                float t[kQuantVec];
+                load8(p + (int64_t)i * kQuantVec, t);
+#pragma unroll
+                for (int c = 0; c < kQuantVec; ++c)
+                    m = max(m, abs_bits(t[c]));
+            }
+        }
+        // magnitudes compare as their bits do; NaN and infinity come out on top
+#pragma unroll
+        for (int d = 1; d < (G < 64 ? G : 64); d <<= 1)
+            m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        if (kWavesPerRow > 1) {
+            if ((tid & 63) == 0)
+                s_max[flip][tid >> 6] = m;
+            __syncthreads();
+            const int w0 = tid / G * kWavesPerRow;
+#pragma unroll
+            for (int w = 0; w < kWavesPerRow; ++w)
+                m = max(m, s_max[flip][w0 + w]);
+            flip ^= 1;
+        }
+        if (!live)
+            continue;
+        float a = __uint_as_float(m), up = 1.0f, s = 1.0f, inv = 0.0f;
+        if (m >= 0x7F800000u) {
+            s = __uint_as_float(0x7FC00000u);
+        } else if (m) {
+            s = a / 127.0f;
+            if (a < 5.42101086e-20f)                          // 2^-64: keep 127 / a finite
+                up = 18446744073709551616.0f;                 // 2^64, exact
+            a *= up;
+            inv = 127.0f / a;
+        }
+        if (g == 0)
+            scale[row] = s;
+        const bool zero = inv == 0.0f;
+        int8_t* out = q + row * H;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (g + i * G < nvec)
+                *reinterpret_cast<u32x2*>(out + (int64_t)(g + i * G) * kQuantVec) =
+                    zero ? u32x2{0u, 0u} : codes8(v[i], a, inv, up);
+        for (int i = g + NV * G; i < nvec; i += G) {
+            float t[kQuantVec];
+            load8(p + (int64_t)i * kQuantVec, t);
+            *reinterpret_cast<u32x2*>(out + (int64_t)i * kQuantVec) =
+                zero ? u32x2{0u, 0u} : codes8(t, a, inv, up);
+        }
+    }
+}
+
+template <typename X, int G, int NV>
+void launch_quant_g(const void* x, int32_t R, int32_t H, const int32_t* n_rows, int8_t* q,
+                    float* scale, hipStream_t stream)
+{
+    constexpr int kThreads = G < 256 ? 256 : G;
+    const int64_t blocks = div_up(R, kThreads / G);
+    const int64_t most = 1 << 20;
+    k_quant_rows<X, G, NV><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, stream>>>(
+        static_cast<const X*>(x), R, H, n_rows, q, scale);
+}
+
+template <typename X>
+void launch_quant(const void* x, int32_t R, int32_t H, const int32_t* n_rows, int8_t* q,
+                  float* scale, hipStream_t stream)
+{
+    if (H <= 16 * 4 * kQuantVec)
+        launch_quant_g<X, 16, 4>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 64 * 4 * kQuantVec)
+        launch_quant_g<X, 64, 4>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 256 * 4 * kQuantVec)
+        launch_quant_g<X, 256, 4>(x, R, H, n_rows, q, scale, stream);
+    else
+        launch_quant_g<X, 1024, 4>(x, R, H, n_rows, q, scale, stream);
+}
+
+// ------------------------------------------------------------------------ experts' product --
+struct MatmulArgs {
+    const int8_t* a;
+    const float* a_scale;
+    const int32_t* row_token;
+    const int8_t* w;
+    const float* w_scale;
+    const int32_t* offsets;
+    void* out;
+    int32_t a_rows, R, E, N, K;
+    int32_t n_blocks;          // workgroups side by side over the channels
+};
+
+// Rows [row0, row0 + rows) of expert e; rows = 0: nothing to do.
+struct Tile {
+    int32_t e, row0, rows;
+};
+
+// The index-th tile of BM rows, counting through the experts (every thread of the workgroup calls).
+// Each thread adds up the tiles of its share of the experts, a scan over the workgroup finds the
+// thread whose share holds the index. Offsets are clamped into [0, R], so no value of theirs leads
+// outside the rows.
+template <int THREADS>
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t BM, int32_t index)
+{
+    __shared__ int32_t s_wave[THREADS / 64];
+    __shared__ Tile s_tile;
+    if (!p.offsets) {
+        const int64_t row0 = (int64_t)index * BM;
+        return Tile{0, (int32_t)min(row0, (int64_t)p.R), (int32_t)max((int64_t)0, min((int64_t)BM, p.R - row0))};
+    }
+    const int tid = threadIdx.x;
+    const int per = (p.E + THREADS - 1) / THREADS;
+    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    int32_t mine = 0;
+    const auto bounds = [&](int e, int32_t* lo) {
+        *lo = min(max(p.offsets[e], 0), p.R);
+        return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
+    };
+    for (int e = e0; e < e1; ++e) {
+        int32_t lo;
+        const int32_t n = bounds(e, &lo);
+        mine += (int32_t)(((int64_t)n + BM - 1) / BM);
+    }
+    int32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_up(upto, d);
+        if ((tid & 63) >= d)
+            upto += o;
+    }
+    if ((tid & 63) == 63)
+        s_wave[tid >> 6] = upto;
+    if (tid == 0)
+        s_tile.rows = 0;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 6); ++w)
+        upto += s_wave[w];
+    int32_t before = upto - mine;
+    if (before <= index && index < upto) {
+        for (int e = e0; e < e1; ++e) {
+            int32_t lo;
+            const int32_t n = bounds(e, &lo);
+            const int32_t tiles = (int32_t)(((int64_t)n + BM - 1) / BM);
+            if (index < before + tiles) {
+                const int32_t at = (index - before) * BM;
+                s_tile = Tile{e, lo + at, min(BM, n - at)};
+                break;
+            }
+            before += tiles;
+        }
+    }
+    __syncthreads();
+    return s_tile;
+}
+
+__device__ __forceinline__ float swiglu(float gate, float up)
+{
+    return gate / (1.0f + expf(-gate)) * up;
+}
+
+__device__ __forceinline__ void store4(float* p, int n, const float v[4])
+{
+    for (int i = 0; i < 4; ++i)
+        if (i < n)
+            p[i] = v[i];
+}
+
+__device__ __forceinline__ void store4(__bf16* p, int n, const float v[4])
+{
+    for (int i = 0; i < 4; ++i)
+        if (i < n)
+            p[i] = (__bf16)v[i];
+}
+
+// Few rows an expert: bound by reading the weights, each once. A workgroup takes up to 16 MF rows
+// of one expert and 16 NF channels; its wavefronts share the K axis out by 128-byte pieces, read
+// weights and rows straight into MFMA operands, and add their int32 sums up through LDS (integers:
+// any order gives the same). v_mfma_i32_16x16x64_i8 with the weights as the left operand: lane l
+// gives channel l % 16 and 16 bytes of K at 16 (l / 16), and gets row l % 16 with channels
+// 4 (l / 16) + i, so that its four results lie side by side in memory.
+template <int MF, int NF, int WAVES, bool SWIGLU, typename OUT>
+__global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
+{
+    __shared__ i32x4 s_acc[WAVES][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int nb = blockIdx.x % p.n_blocks;
+    const Tile tile = find_tile<64 * WAVES>(p, 16 * MF, blockIdx.x / p.n_blocks);
+    if (tile.rows == 0)
+        return;
+    const int r16 = lane & 15, kq = lane >> 4;
+    const int32_t n_w = SWIGLU ? 2 * p.N : p.N;               // channels of w
+    const int8_t* we = p.w + (int64_t)tile.e * n_w * p.K;
+
+    // channels: fragment f covers 16 from n0 + 16 f; with SwiGLU even fragments hold the gate and
+    // the odd ones the same channels' up
+    const int32_t n0 = nb * (SWIGLU ? 8 * NF : 16 * NF);
+    const int8_t* wp[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        int32_t n = SWIGLU ? n0 + 16 * (f / 2) + r16 : n0 + 16 * f + r16;
+        n = min(n, p.N - 1) + (SWIGLU && (f & 1) ? p.N : 0);
+        wp[f] = we + (int64_t)n * p.K;
+    }
+    const int8_t* ap[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const int32_t r = tile.row0 + min(16 * m + r16, tile.rows - 1);
+        int32_t src = p.row_token ? p.row_token[r] : r;
+        src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
+        ap[m] = p.a + (int64_t)src * p.K;
+    }
+    i32x4 acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            acc[m][f] = i32x4{0, 0, 0, 0};
+
+    for (int32_t k0 = wave * 128; k0 < p.K; k0 += WAVES * 128) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int32_t at = k0 + 64 * h + 16 * kq;
+            const bool in = at < p.K;                         // K is a multiple of 16
+            i32x4 wv[NF], av[MF];
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                wv[f] = in ? *reinterpret_cast<const i32x4*>(wp[f] + at) : i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                av[m] = in ? *reinterpret_cast<const i32x4*>(ap[m] + at) : i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[m][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[f], av[m], acc[m][f], 0,
+                                                                      0, 0);
+        }
+    }
+    // join the wavefronts, fragment by fragment
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            __syncthreads();
+            s_acc[wave][lane] = acc[m][f];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < WAVES; ++w)
+                    acc[m][f] += s_acc[w][lane];
+            }
+        }
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const int32_t at = 16 * m + r16;
+        if (at >= tile.rows)
+            continue;
+        const int32_t r = tile.row0 + at;
+        const int32_t src = p.row_token ? p.row_token[r] : r;
+        if ((uint32_t)src >= (uint32_t)p.a_rows)
+            continue;
+        const float sa = p.a_scale[src];
+        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N;
+#pragma unroll
+        for (int f = 0; f < NF; f += SWIGLU ? 2 : 1) {
+            const int32_t n = (SWIGLU ? n0 + 8 * f : n0 + 16 * f) + 4 * kq;
+            const int32_t left = p.N - n;
+            if (left <= 0)
+                continue;
+            const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = i < left ? i : 0;
+                v[i] = (float)acc[m][f][i] * sa * sw[o];
+                if (SWIGLU)
+                    v[i] = swiglu(v[i], (float)acc[m][f + (SWIGLU ? 1 : 0)][i] * sa * sw[p.N + o]);
+            }
+            store4(out + n, left, v);
+        }
+    }
+}
+
+template <int MF, int NF, int WAVES, bool SWIGLU, typename OUT>
+void launch_few(MatmulArgs p, hipStream_t stream)
+{
+    p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
+    const int64_t tiles = p.offsets ? p.R / (16 * MF) + (p.E < p.R ? p.E : p.R) : div_up(p.R, 16 * MF);
+    k_matmul_few<MF, NF, WAVES, SWIGLU, OUT><<<(unsigned)(tiles * p.n_blocks), 64 * WAVES, 0,
+                                               stream>>>(p);
+}
+
+template <bool SWIGLU, typename OUT>
+void launch_matmul(const MatmulArgs& p, hipStream_t stream)
+{
+    launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
+}
+
+moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quant_rows(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t H,
+                            const int32_t* n_rows, int8_t* q, float* scale, hipStream_t stream)
+{
+    if (R < 0 || H < 1)
+        return MOE_ERR_INVALID;
+    if ((x_dtype != MOE_F32 && x_dtype != MOE_BF16) || H % 16 != 0)
+        return MOE_ERR_UNSUPPORTED;
+    if (R > 0 && (!x || !q || !scale))
+        return MOE_ERR_INVALID;
+    if (!aligned_to((const char*)x, 16) || !aligned_to(q, 16) || !aligned_to(scale, 4))
+        return MOE_ERR_UNSUPPORTED;
+    if (R == 0)
+        return MOE_OK;
+    if (x_dtype == MOE_BF16)
+        launch_quant<uint16_t>(x, R, H, n_rows, q, scale, stream);
+    else
+        launch_quant<float>(x, R, H, n_rows, q, scale, stream);
+    return launched();
+}
+
+moe_status_t moe_expert_matmul_i8(const int8_t* a, const float* a_scale, int32_t a_rows,
+                                  const int32_t* row_token, const int8_t* w, const float* w_scale,
+                                  const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
+                                  int32_t K, moe_act_t act, void* out, moe_dtype_t out_dtype,
+                                  hipStream_t stream)
+{
+    if (R < 0 || a_rows < 0 || E < 1 || N < 1 || K < 1 ||
+        (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) || (!expert_offsets && E != 1) ||
+        (!row_token && R > a_rows) || (row_token && R > 0 && a_rows < 1))
+        return MOE_ERR_INVALID;
+    const int64_t n_w = act == MOE_ACT_SWIGLU ? 2 * (int64_t)N : N;
+    if ((out_dtype != MOE_F32 && out_dtype != MOE_BF16) || K % 16 != 0 || K > MOE_MATMUL_MAX_K ||
+        E > MOE_MAX_EXPERTS || n_w * K >= ((int64_t)1 << 32) ||
+        (row_token && (int64_t)a_rows * K >= ((int64_t)1 << 32)))
+        return MOE_ERR_UNSUPPORTED;
+    if (R > 0 && (!a || !a_scale || !w || !w_scale || !out))
+        return MOE_ERR_INVALID;
+    if (!aligned_to(a, 16) || !aligned_to(w, 16) ||
+        !aligned_to((const char*)out, out_dtype == MOE_F32 ? 4 : 2))
+        return MOE_ERR_UNSUPPORTED;
+    if (R == 0)
+        return MOE_OK;
+    MatmulArgs p;
+    p.a = a;
+    p.a_scale = a_scale;
+    p.row_token = row_token;
+    p.w = w;
+    p.w_scale = w_scale;
+    p.offsets = expert_offsets;
+    p.out = out;
+    p.a_rows = a_rows;
+    p.R = R;
+    p.E = E;
+    p.N = N;
+    p.K = K;
+    p.n_blocks = 0;
+    if (act == MOE_ACT_SWIGLU) {
+        if (out_dtype == MOE_BF16)
+            launch_matmul<true, __bf16>(p, stream);
+        else
+            launch_matmul<true, float>(p, stream);
+    } else {
+        if (out_dtype == MOE_BF16)
+            launch_matmul<false, __bf16>(p, stream);
+        else
+            launch_matmul<false, float>(p, stream);
+    }
+    return launched();
+}
+
+}  // extern "C"
