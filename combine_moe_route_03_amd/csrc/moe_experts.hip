@@ -13,6 +13,7 @@ using namespace moe_dev;
 // for an element. G lanes take a row, with up to NV vectors of 8 elements a lane; longer rows are
 // read a second time, from the cache.
 constexpr int kQuantVec = 8;
+constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
 
 template <typename X>
 __device__ __forceinline__ void load8(const X* __restrict__ p, float v[8]);
@@ -195,36 +196,40 @@ struct MatmulArgs {
     int32_t n_blocks;          // workgroups side by side over the channels
 };
 
-// Rows [row0, row0 + rows) of expert e; rows = 0: nothing to do.
+// Rows [row0, row0 + rows) of expert e, channel block n; rows = 0: nothing to do.
 struct Tile {
-    int32_t e, row0, rows;
+    int32_t e, row0, rows, n;
 };
 
-// The index-th tile of BM rows, counting through the experts (every thread of the workgroup calls).
-// Each thread adds up the tiles of its share of the experts, a scan over the workgroup finds the
-// thread whose share holds the index. Offsets are clamped into [0, R], so no value of theirs leads
-// outside the rows.
-template <int THREADS>
-__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t BM, int32_t index)
+// The tile of workgroup blockIdx.x (every thread calls): tiles of BM rows by p.n_blocks channel
+// blocks, expert by expert. Each thread adds up the row tiles of its share of the experts, a scan
+// over the workgroup gives the total and finds the thread whose share holds the workgroup's tile.
+// The host only knows a bound of the total, so workgroups beyond it have nothing to do. Offsets are
+// clamped into [0, R], so no value of theirs leads outside the rows.
+//   Workgroup b runs on XCD b % 8: an XCD takes a run of consecutive tiles, GROUP row tiles by all
+// channel blocks at a time (row tiles fastest), so that the workgroups that run together on it
+// share weights and rows in its L2.
+template <int THREADS, int BM, int GROUP>
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p)
 {
     __shared__ int32_t s_wave[THREADS / 64];
-    __shared__ Tile s_tile;
-    if (!p.offsets) {
-        const int64_t row0 = (int64_t)index * BM;
-        return Tile{0, (int32_t)min(row0, (int64_t)p.R), (int32_t)max((int64_t)0, min((int64_t)BM, p.R - row0))};
-    }
+    __shared__ int32_t s_found[3];
     const int tid = threadIdx.x;
     const int per = (p.E + THREADS - 1) / THREADS;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
-    int32_t mine = 0;
-    const auto bounds = [&](int e, int32_t* lo) {
+    const auto rows_of = [&](int e, int32_t* lo) {
+        if (!p.offsets) {
+            *lo = 0;
+            return p.R;
+        }
         *lo = min(max(p.offsets[e], 0), p.R);
         return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
     };
+    const auto tiles_of = [](int32_t n) { return n / BM + (n % BM != 0); };
+    int32_t mine = 0;
     for (int e = e0; e < e1; ++e) {
         int32_t lo;
-        const int32_t n = bounds(e, &lo);
-        mine += (int32_t)(((int64_t)n + BM - 1) / BM);
+        mine += tiles_of(rows_of(e, &lo));
     }
     int32_t upto = mine;
 #pragma unroll
@@ -235,27 +240,50 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t BM, int32
     }
     if ((tid & 63) == 63)
         s_wave[tid >> 6] = upto;
-    if (tid == 0)
-        s_tile.rows = 0;
     __syncthreads();
-    for (int w = 0; w < (tid >> 6); ++w)
-        upto += s_wave[w];
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < (tid >> 6))
+            upto += s_wave[w];
+        total += s_wave[w];
+    }
+    const int64_t all = (int64_t)total * p.n_blocks;
+    const int64_t share = (all + kXcds - 1) / kXcds;
+    const int64_t at = (int64_t)(blockIdx.x % kXcds) * share + blockIdx.x / kXcds;
+    if (blockIdx.x / kXcds >= share || at >= all)
+        return Tile{0, 0, 0, 0};                              // the same for the whole workgroup
+    const int64_t index = at / p.n_blocks;                    // a row tile of the same expert
     int32_t before = upto - mine;
     if (before <= index && index < upto) {
         for (int e = e0; e < e1; ++e) {
             int32_t lo;
-            const int32_t n = bounds(e, &lo);
-            const int32_t tiles = (int32_t)(((int64_t)n + BM - 1) / BM);
+            const int32_t tiles = tiles_of(rows_of(e, &lo));
             if (index < before + tiles) {
-                const int32_t at = (index - before) * BM;
-                s_tile = Tile{e, lo + at, min(BM, n - at)};
+                s_found[0] = e;
+                s_found[1] = before;
+                s_found[2] = tiles;
                 break;
             }
             before += tiles;
         }
     }
     __syncthreads();
-    return s_tile;
+    Tile tile;
+    tile.e = __builtin_amdgcn_readfirstlane(s_found[0]);
+    before = __builtin_amdgcn_readfirstlane(s_found[1]);
+    const int32_t tiles = __builtin_amdgcn_readfirstlane(s_found[2]);
+    const int64_t local = at - (int64_t)before * p.n_blocks;
+    const int32_t group = (int32_t)(local / ((int64_t)GROUP * p.n_blocks));
+    const int32_t in = (int32_t)(local - (int64_t)group * GROUP * p.n_blocks);
+    const int32_t side = min(GROUP, tiles - group * GROUP);
+    tile.n = in / side;
+    const int32_t m = group * GROUP + in % side;
+    int32_t lo;
+    const int32_t n = rows_of(tile.e, &lo);
+    tile.row0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
+    tile.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
+    return tile;
 }
 
 __device__ __forceinline__ float swiglu(float gate, float up)
@@ -288,10 +316,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
 {
     __shared__ i32x4 s_acc[WAVES][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int nb = blockIdx.x % p.n_blocks;
-    const Tile tile = find_tile<64 * WAVES>(p, 16 * MF, blockIdx.x / p.n_blocks);
+    const Tile tile = find_tile<64 * WAVES, 16 * MF, 4>(p);
     if (tile.rows == 0)
         return;
+    const int nb = tile.n;
     const int r16 = lane & 15, kq = lane >> 4;
     const int32_t n_w = SWIGLU ? 2 * p.N : p.N;               // channels of w
     const int8_t* we = p.w + (int64_t)tile.e * n_w * p.K;
@@ -388,19 +416,246 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
     }
 }
 
+// ---- many rows an expert ----
+// LDS stages of BM rows and BN channels, 128 bytes of K each, filled by loads that go straight to
+// LDS. A wavefront's load brings 8 lines of 128 bytes: lane l the 16-byte piece (l % 8) ^ (l / 8)
+// of line l / 8, so that piece c of line r lies in slot c ^ (r % 8) and the operand reads (the same
+// piece of consecutive lines) fall on different banks.
+constexpr int kStepK = 128;
+
+__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    u32x4 r;
+    r[0] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    r[1] = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu));
+    r[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
+    r[3] = 0x00020000u;
+    return r;
+}
+
+// 16 bytes a lane from `buffer` at voff + soff to LDS at lds + 16 * lane. In asm, since the
+// compiler would wait for all such loads before every LDS read; it has no register output, and
+// wait_stage() waits for it.
+__device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
+}
+
+// All but the PENDING youngest of this wavefront's loads are in LDS, its LDS reads are done, and so
+// it is for the other wavefronts of the workgroup.
+template <int PENDING>
+__device__ __forceinline__ void wait_stage()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(PENDING) : "memory");
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, typename OUT>
+__global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
+{
+    constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    constexpr int MF = BM / WM / 32, NF = BN / WN / 32;       // 32 x 32 fragments of a wavefront
+    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;
+    constexpr int kLoads = kLoadsA + kLoadsW;
+    constexpr int kStage = (BM + BN) * kStepK;
+    static_assert(MF * WM * 32 == BM && NF * WN * 32 == BN, "tile");
+    static_assert(kLoadsA * 8 * kWaves == BM && kLoadsW * 8 * kWaves == BN, "loads");
+    static_assert(!SWIGLU || NF % 2 == 0, "gate and up in one wavefront");
+    extern __shared__ __attribute__((aligned(1024))) int8_t s_stage[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Tile tile = find_tile<kThreads, BM, 4>(p);
+    if (tile.rows == 0)
+        return;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)s_stage;
+    const int32_t n_w = SWIGLU ? 2 * p.N : p.N;
+    const int32_t n0 = tile.n * (SWIGLU ? BN / 2 : BN);
+    const int8_t* we = p.w + (int64_t)tile.e * n_w * p.K;
+    const u32x4 wbuf = buffer_of(we, (uint32_t)((int64_t)n_w * p.K));
+    const u32x4 abuf = p.row_token
+                           ? buffer_of(p.a, (uint32_t)((int64_t)p.a_rows * p.K))
+                           : buffer_of(p.a + (int64_t)tile.row0 * p.K,
+                                       (uint32_t)(tile.rows * p.K));
+
+    // this lane's pieces: line 8 (i waves + wave) + l / 8 of the rows, and of the channels
+    const int line = lane >> 3, piece = 16 * ((lane & 7) ^ line);
+    uint32_t avo[kLoadsA], wvo[kLoadsW];
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) {
+        const int32_t m = min(8 * (i * kWaves + wave) + line, tile.rows - 1);
+        int32_t src = m;
+        if (p.row_token) {
+            src = p.row_token[tile.row0 + m];
+            src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
+        }
+        avo[i] = (uint32_t)src * (uint32_t)p.K + piece;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i) {
+        const int32_t c = 8 * (i * kWaves + wave) + line;
+        // with SwiGLU every other 32 channels are the up channels of the 32 before
+        int32_t n = SWIGLU ? n0 + c / 64 * 32 + c % 32 : n0 + c;
+        n = min(n, p.N - 1) + (SWIGLU && (c & 32) ? p.N : 0);
+        wvo[i] = (uint32_t)n * (uint32_t)p.K + piece;
+    }
+    const int32_t steps = (p.K + kStepK - 1) / kStepK;
+    const auto issue = [&](int32_t step) {
+        const uint32_t at = (uint32_t)step * kStepK;
+        const uint32_t to = lds0 + (uint32_t)(step % STAGES) * kStage + wave * 1024;
+        // pieces behind the end of K repeat the step's first one; their products are zeroed
+        const uint32_t back = at + piece >= (uint32_t)p.K ? piece : 0u;
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i)
+            load_lds(abuf, avo[i] - back, at, to + i * kWaves * 1024);
+#pragma unroll
+        for (int i = 0; i < kLoadsW; ++i)
+            load_lds(wbuf, wvo[i] - back, at, to + BM * kStepK + i * kWaves * 1024);
+    };
+
+    const int wm = wave % WM, wn = wave / WM;
+    const int r32 = lane & 31, half = lane >> 5;
+    typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+    i32x16 acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[m][f][i] = 0;
+    // this lane's slots of the four 32-byte quarters of a step
+    int slot[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        slot[q] = r32 * kStepK + 16 * ((2 * q + half) ^ (r32 & 7));
+    // whole: the step has all of its 128 bytes; else pieces behind the end of K count as zeros
+    const auto compute = [&](int32_t step, bool whole) {
+        const int base = (step % STAGES) * kStage + wm * MF * 32 * kStepK;
+        const int basew = (step % STAGES) * kStage + (BM + wn * NF * 32) * kStepK;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            i32x4 wv[NF], av[MF];
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                wv[f] = *reinterpret_cast<const i32x4*>(s_stage + (basew + slot[q]) + f * 32 * kStepK);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                av[m] = *reinterpret_cast<const i32x4*>(s_stage + (base + slot[q]) + m * 32 * kStepK);
+            if (!whole && step * kStepK + 16 * (2 * q + half) >= p.K) {
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    av[m] = i32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[f], av[m], acc[m][f], 0,
+                                                                      0, 0);
+        }
+    };
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < steps)
+            issue(s);
+    const int32_t whole = p.K / kStepK;
+    for (int32_t step = 0; step < whole; ++step) {
+        if (step + STAGES - 2 < steps)
+            wait_stage<(STAGES - 2) * kLoads>();
+        else
+            wait_stage<0>();
+        if (step + STAGES - 1 < steps)
+            issue(step + STAGES - 1);
+        compute(step, true);
+    }
+    if (whole < steps) {
+        wait_stage<0>();
+        compute(whole, false);
+    }
+
+    // lane l has row l % 32 of a fragment and its channels 8 (i / 4) + 4 (l / 32) + i % 4
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const int32_t at = (wm * MF + m) * 32 + r32;
+        if (at >= tile.rows)
+            continue;
+        const int32_t r = tile.row0 + at;
+        const int32_t src = p.row_token ? p.row_token[r] : r;
+        if ((uint32_t)src >= (uint32_t)p.a_rows)
+            continue;
+        const float sa = p.a_scale[src];
+        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N;
+#pragma unroll
+        for (int f = 0; f < NF; f += SWIGLU ? 2 : 1) {
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const int32_t c = (wn * NF + f) * 32;
+                const int32_t n = n0 + (SWIGLU ? c / 2 : c) + 8 * i4 + 4 * half;
+                const int32_t left = p.N - n;
+                if (left <= 0)
+                    continue;
+                const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int o = i < left ? i : 0;
+                    v[i] = (float)acc[m][f][4 * i4 + i] * sa * sw[o];
+                    if (SWIGLU)
+                        v[i] = swiglu(v[i], (float)acc[m][f + (SWIGLU ? 1 : 0)][4 * i4 + i] * sa *
+                                                sw[p.N + o]);
+                }
+                store4(out + n, left, v);
+            }
+        }
+    }
+}
+
+// Workgroups for tiles of bm rows: the row tiles of all experts are at most R / bm and one more for
+// each expert that has rows.
+inline int64_t most_tiles(const MatmulArgs& p, int32_t bm)
+{
+    return p.offsets ? p.R / bm + (p.E < p.R ? p.E : p.R) : div_up(p.R, bm);
+}
+
 template <int MF, int NF, int WAVES, bool SWIGLU, typename OUT>
-void launch_few(MatmulArgs p, hipStream_t stream)
+bool launch_few(MatmulArgs p, hipStream_t stream)
 {
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
-    const int64_t tiles = p.offsets ? p.R / (16 * MF) + (p.E < p.R ? p.E : p.R) : div_up(p.R, 16 * MF);
-    k_matmul_few<MF, NF, WAVES, SWIGLU, OUT><<<(unsigned)(tiles * p.n_blocks), 64 * WAVES, 0,
-                                               stream>>>(p);
+    const int64_t blocks = div_up(most_tiles(p, 16 * MF) * p.n_blocks, kXcds) * kXcds;
+    if (blocks * 64 * WAVES > INT32_MAX)
+        return false;
+    k_matmul_few<MF, NF, WAVES, SWIGLU, OUT><<<(unsigned)blocks, 64 * WAVES, 0, stream>>>(p);
+    return true;
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, typename OUT>
+bool launch_tile(MatmulArgs p, hipStream_t stream)
+{
+    constexpr int kThreads = 64 * WM * WN, kLds = STAGES * (BM + BN) * kStepK;
+    p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? BN / 2 : BN);
+    const int64_t blocks = div_up(most_tiles(p, BM) * p.n_blocks, kXcds) * kXcds;
+    if (blocks * kThreads > INT32_MAX)
+        return false;
+    const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, SWIGLU, OUT>;
+    if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
+                                            hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            kLds) != hipSuccess)
+        return false;
+    kernel<<<(unsigned)blocks, kThreads, kLds, stream>>>(p);
+    return true;
 }
 
 template <bool SWIGLU, typename OUT>
-void launch_matmul(const MatmulArgs& p, hipStream_t stream)
+bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
 {
-    launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
+    const int64_t rows = p.R / p.E;                           // of an expert, on average
+    if (rows < 32)
+        return launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
+    if (rows < 160)
+        return launch_tile<128, 256, 2, 4, 3, SWIGLU, OUT>(p, stream);
+    return launch_tile<256, 256, 2, 4, 2, SWIGLU, OUT>(p, stream);
 }
 
 moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
@@ -465,18 +720,12 @@ moe_status_t moe_expert_matmul_i8(const int8_t* a, const float* a_scale, int32_t
     p.N = N;
     p.K = K;
     p.n_blocks = 0;
-    if (act == MOE_ACT_SWIGLU) {
-        if (out_dtype == MOE_BF16)
-            launch_matmul<true, __bf16>(p, stream);
-        else
-            launch_matmul<true, float>(p, stream);
-    } else {
-        if (out_dtype == MOE_BF16)
-            launch_matmul<false, __bf16>(p, stream);
-        else
-            launch_matmul<false, float>(p, stream);
-    }
-    return launched();
+    const bool bf16 = out_dtype == MOE_BF16;
+    const bool fits = act == MOE_ACT_SWIGLU ? (bf16 ? launch_matmul<true, __bf16>(p, stream)
+                                                    : launch_matmul<true, float>(p, stream))
+                                            : (bf16 ? launch_matmul<false, __bf16>(p, stream)
+                                                    : launch_matmul<false, float>(p, stream));
+    return fits ? launched() : MOE_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"
