@@ -14,6 +14,7 @@ using namespace moe_dev;
 // read a second time, from the cache.
 constexpr int kQuantVec = 8;
 constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
+constexpr int kCus = 256;
 
 template <typename X>
 __device__ __forceinline__ void load8(const X* __restrict__ p, float v[8]);
@@ -417,10 +418,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
 }
 
 // ---- many rows an expert ----
-// LDS stages of BM rows and BN channels, 128 bytes of K each, filled by loads that go straight to
-// LDS. A wavefront's load brings 8 lines of 128 bytes: lane l the 16-byte piece (l % 8) ^ (l / 8)
-// of line l / 8, so that piece c of line r lies in slot c ^ (r % 8) and the operand reads (the same
-// piece of consecutive lines) fall on different banks.
+// Persistent workgroups, one a CU, take tiles of BM rows by BN channels. K goes through LDS stages
+// of 128 bytes a row, filled by loads that go straight to LDS. A wavefront's load brings 8 lines of
+// 128 bytes: lane l the 16-byte piece (l % 8) ^ (l / 8) of line l / 8, so that piece c of line r
+// lies in slot c ^ (r % 8) and the operand reads (the same piece of consecutive lines) fall on
+// different banks. Operands of a quarter step are read while the quarter before is multiplied.
 constexpr int kStepK = 128;
 
 __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
@@ -436,19 +438,123 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
 
 // 16 bytes a lane from `buffer` at voff + soff to LDS at lds + 16 * lane. In asm, since the
 // compiler would wait for all such loads before every LDS read; it has no register output, and
-// wait_stage() waits for it.
+// wait_loads() waits for it.
 __device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
 }
 
-// All but the PENDING youngest of this wavefront's loads are in LDS, its LDS reads are done, and so
-// it is for the other wavefronts of the workgroup.
+// All but the PENDING youngest of this wavefront's loads are in LDS.
 template <int PENDING>
-__device__ __forceinline__ void wait_stage()
+__device__ __forceinline__ void wait_loads()
 {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(PENDING) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(PENDING) : "memory");
+}
+
+// This wavefront's LDS accesses are done, and so are those of the others of the workgroup.
+__device__ __forceinline__ void wait_workgroup()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ void store8(float* p, const float v[8])
+{
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+__device__ __forceinline__ void store8(__bf16* p, const float v[8])
+{
+    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+    bf16x8 b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        b[i] = (__bf16)v[i];
+    *reinterpret_cast<bf16x8*>(p) = b;
+}
+
+// Exclusive prefix of the experts' row tiles into prefix[0 .. E] (every thread calls), and their
+// total. Offsets are clamped into [0, R], so no value of theirs leads outside the rows.
+__device__ __forceinline__ int32_t expert_rows(const MatmulArgs& p, int32_t e, int32_t* lo)
+{
+    if (!p.offsets) {
+        *lo = 0;
+        return p.R;
+    }
+    *lo = min(max(p.offsets[e], 0), p.R);
+    return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
+}
+
+template <int THREADS, int BM>
+__device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* prefix)
+{
+    __shared__ int32_t s_wave[THREADS / 64];
+    const int tid = threadIdx.x;
+    const int per = (p.E + THREADS - 1) / THREADS;
+    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    const auto tiles = [&](int32_t e) {
+        int32_t lo;
+        const int32_t n = expert_rows(p, e, &lo);
+        return n / BM + (n % BM != 0);
+    };
+    int32_t mine = 0;
+    for (int e = e0; e < e1; ++e)
+        mine += tiles(e);
+    int32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t o = __shfl_up(upto, d);
+        if ((tid & 63) >= d)
+            upto += o;
+    }
+    if ((tid & 63) == 63)
+        s_wave[tid >> 6] = upto;
+    __syncthreads();
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < (tid >> 6))
+            upto += s_wave[w];
+        total += s_wave[w];
+    }
+    int32_t at = upto - mine;
+    for (int e = e0; e < e1; ++e) {
+        prefix[e] = at;
+        at += tiles(e);
+    }
+    if (tid == 0)
+        prefix[p.E] = total;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+// Tile `at` of all: expert by expert, GROUP row tiles by all channel blocks at a time, row tiles
+// fastest, so that tiles that run together on an XCD share weights and rows in its L2.
+template <int BM, int GROUP>
+__device__ __forceinline__ Tile tile_at(const MatmulArgs& p, const int32_t* prefix, int32_t at)
+{
+    const int32_t index = at / p.n_blocks;
+    int32_t e = -1;
+    for (int j = 0; j < p.E; j += 64) {
+        const int i = j + (threadIdx.x & 63);
+        e += __popcll(__ballot(i < p.E && prefix[i] <= index));
+    }
+    const int32_t before = __builtin_amdgcn_readfirstlane(prefix[e]);
+    const int32_t tiles = __builtin_amdgcn_readfirstlane(prefix[e + 1]) - before;
+    const int32_t local = at - before * p.n_blocks;
+    const int32_t group = local / (GROUP * p.n_blocks);
+    const int32_t in = local - group * GROUP * p.n_blocks;
+    const int32_t side = min(GROUP, tiles - group * GROUP);
+    Tile t;
+    t.e = e;
+    t.n = in / side;
+    const int32_t m = group * GROUP + in % side;
+    int32_t lo;
+    const int32_t n = expert_rows(p, e, &lo);
+    t.row0 = lo + m * BM;
+    t.rows = min(BM, n - m * BM);
+    return t;
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, typename OUT>
@@ -459,156 +565,273 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;
     constexpr int kLoads = kLoadsA + kLoadsW;
     constexpr int kStage = (BM + BN) * kStepK;
+    constexpr int kGroup = 4;
     static_assert(MF * WM * 32 == BM && NF * WN * 32 == BN, "tile");
     static_assert(kLoadsA * 8 * kWaves == BM && kLoadsW * 8 * kWaves == BN, "loads");
-    static_assert(!SWIGLU || NF % 2 == 0, "gate and up in one wavefront");
+    static_assert(NF % 2 == 0 && kWaves * 8192 <= kStage && STAGES >= 2, "pairs of fragments");
     extern __shared__ __attribute__((aligned(1024))) int8_t s_stage[];
+    __shared__ int32_t s_prefix[MOE_MAX_EXPERTS + 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Tile tile = find_tile<kThreads, BM, 4>(p);
-    if (tile.rows == 0)
+    const int32_t all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
+    // workgroup b runs on XCD b % 8: each XCD takes a run of consecutive tiles
+    const int32_t share = (all + kXcds - 1) / kXcds;
+    const int32_t stride = gridDim.x / kXcds;
+    const int32_t first = (blockIdx.x % kXcds) * share + blockIdx.x / kXcds;
+    const int32_t last = min((int32_t)(blockIdx.x % kXcds + 1) * share, all);
+    if (first >= last)
         return;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)s_stage;
     const int32_t n_w = SWIGLU ? 2 * p.N : p.N;
-    const int32_t n0 = tile.n * (SWIGLU ? BN / 2 : BN);
-    const int8_t* we = p.w + (int64_t)tile.e * n_w * p.K;
-    const u32x4 wbuf = buffer_of(we, (uint32_t)((int64_t)n_w * p.K));
-    const u32x4 abuf = p.row_token
-                           ? buffer_of(p.a, (uint32_t)((int64_t)p.a_rows * p.K))
-                           : buffer_of(p.a + (int64_t)tile.row0 * p.K,
-                                       (uint32_t)(tile.rows * p.K));
-
-    // this lane's pieces: line 8 (i waves + wave) + l / 8 of the rows, and of the channels
-    const int line = lane >> 3, piece = 16 * ((lane & 7) ^ line);
-    uint32_t avo[kLoadsA], wvo[kLoadsW];
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-        const int32_t m = min(8 * (i * kWaves + wave) + line, tile.rows - 1);
-        int32_t src = m;
-        if (p.row_token) {
-            src = p.row_token[tile.row0 + m];
-            src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
-        }
-        avo[i] = (uint32_t)src * (uint32_t)p.K + piece;
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsW; ++i) {
-        const int32_t c = 8 * (i * kWaves + wave) + line;
-        // with SwiGLU every other 32 channels are the up channels of the 32 before
-        int32_t n = SWIGLU ? n0 + c / 64 * 32 + c % 32 : n0 + c;
-        n = min(n, p.N - 1) + (SWIGLU && (c & 32) ? p.N : 0);
-        wvo[i] = (uint32_t)n * (uint32_t)p.K + piece;
-    }
     const int32_t steps = (p.K + kStepK - 1) / kStepK;
-    const auto issue = [&](int32_t step) {
-        const uint32_t at = (uint32_t)step * kStepK;
-        const uint32_t to = lds0 + (uint32_t)(step % STAGES) * kStage + wave * 1024;
-        // pieces behind the end of K repeat the step's first one; their products are zeroed
-        const uint32_t back = at + piece >= (uint32_t)p.K ? piece : 0u;
+    const bool ragged = p.K % kStepK != 0;
+
+    // The loads run ahead of the products through the same tiles: their own place in them
+    const int line = lane >> 3, piece = 16 * ((lane & 7) ^ line);
+    const bool behind = (p.K & ~(kStepK - 1)) + piece >= p.K; // in a ragged last step
+    u32x4 abuf, wbuf;
+    uint32_t avo[kLoadsA], wvo[kLoadsW];
+    int32_t load_tile = first, load_step = 0;
+    uint32_t load_to = lds0 + wave * 1024;
+    int32_t ahead = 0;                                        // stages loaded and not yet begun
+    const auto aim = [&]() {
+        const Tile t = tile_at<BM, kGroup>(p, s_prefix, load_tile);
+        abuf = p.row_token ? buffer_of(p.a, (uint32_t)((int64_t)p.a_rows * p.K))
+                           : buffer_of(p.a + (int64_t)t.row0 * p.K, (uint32_t)(t.rows * p.K));
+        wbuf = buffer_of(p.w + (int64_t)t.e * n_w * p.K, (uint32_t)((int64_t)n_w * p.K));
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i) {
+            const int32_t m = min(8 * (i * kWaves + wave) + line, t.rows - 1);
+            int32_t src = m;
+            if (p.row_token) {
+                src = p.row_token[t.row0 + m];
+                src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
+            }
+            avo[i] = (uint32_t)src * (uint32_t)p.K + piece;
+        }
+        const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
+#pragma unroll
+        for (int i = 0; i < kLoadsW; ++i) {
+            const int32_t c = 8 * (i * kWaves + wave) + line;
+            // with SwiGLU every other 32 channels are the up channels of the 32 before
+            int32_t n = SWIGLU ? n0 + c / 64 * 32 + c % 32 : n0 + c;
+            n = min(n, p.N - 1) + (SWIGLU && (c & 32) ? p.N : 0);
+            wvo[i] = (uint32_t)n * (uint32_t)p.K + piece;
+        }
+    };
+    const auto issue = [&]() {
+        if (load_tile >= last)
+            return;
+        const uint32_t at = (uint32_t)load_step * kStepK;
+        // pieces behind the end of K repeat the step's first one, and are zeroed in LDS later
+        const uint32_t back = ragged && load_step == steps - 1 && behind ? piece : 0u;
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i)
-            load_lds(abuf, avo[i] - back, at, to + i * kWaves * 1024);
+            load_lds(abuf, avo[i] - back, at, load_to + i * kWaves * 1024);
 #pragma unroll
         for (int i = 0; i < kLoadsW; ++i)
-            load_lds(wbuf, wvo[i] - back, at, to + BM * kStepK + i * kWaves * 1024);
+            load_lds(wbuf, wvo[i] - back, at, load_to + BM * kStepK + i * kWaves * 1024);
+        load_to += kStage;
+        if (load_to >= lds0 + STAGES * kStage)
+            load_to -= STAGES * kStage;
+        ++ahead;
+        if (++load_step == steps) {
+            load_step = 0;
+            load_tile += stride;
+            if (load_tile < last)
+                aim();
+        }
     };
 
     const int wm = wave % WM, wn = wave / WM;
     const int r32 = lane & 31, half = lane >> 5;
     typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
     i32x16 acc[MF][NF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                acc[m][f][i] = 0;
     // this lane's slots of the four 32-byte quarters of a step
     int slot[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         slot[q] = r32 * kStepK + 16 * ((2 * q + half) ^ (r32 & 7));
-    // whole: the step has all of its 128 bytes; else pieces behind the end of K count as zeros
-    const auto compute = [&](int32_t step, bool whole) {
-        const int base = (step % STAGES) * kStage + wm * MF * 32 * kStepK;
-        const int basew = (step % STAGES) * kStage + (BM + wn * NF * 32) * kStepK;
+    int at = 0;                                               // the stage that is multiplied
+    i32x4 wv[2][NF], av[2][MF];
+    const auto read = [&](int set, int q) {
+        const int8_t* sw = s_stage + at + (BM + wn * NF * 32) * kStepK + slot[q];
+        const int8_t* sa = s_stage + at + wm * MF * 32 * kStepK + slot[q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            i32x4 wv[NF], av[MF];
+        for (int f = 0; f < NF; ++f)
+            wv[set][f] = *reinterpret_cast<const i32x4*>(sw + f * 32 * kStepK);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+            av[set][m] = *reinterpret_cast<const i32x4*>(sa + m * 32 * kStepK);
+    };
+    const auto multiply = [&](int set) {
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                wv[f] = *reinterpret_cast<const i32x4*>(s_stage + (basew + slot[q]) + f * 32 * kStepK);
+                acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][f], av[set][m],
+                                                                  acc[m][f], 0, 0, 0);
+    };
+    // this wavefront's loads of the next stage have landed; `partial`: it is a ragged last step
+    const auto landed = [&](int32_t next, bool partial) {
+        if (ahead >= STAGES - 1)
+            wait_loads<(STAGES - 2) * kLoads>();
+        else
+            wait_loads<0>();
+        if (partial && behind) {
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
-                av[m] = *reinterpret_cast<const i32x4*>(s_stage + (base + slot[q]) + m * 32 * kStepK);
-            if (!whole && step * kStepK + 16 * (2 * q + half) >= p.K) {
-#pragma unroll
-                for (int m = 0; m < MF; ++m)
-                    av[m] = i32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int m = 0; m < MF; ++m)
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[f], av[m], acc[m][f], 0,
-                                                                      0, 0);
+            for (int i = 0; i < kLoadsA; ++i)
+                *reinterpret_cast<i32x4*>(s_stage + next + (i * kWaves + wave) * 1024 + 16 * lane) =
+                    i32x4{0, 0, 0, 0};
         }
     };
+    const auto after = [&](int stage) { return stage + kStage == STAGES * kStage ? 0 : stage + kStage; };
 
+    aim();
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < steps)
-            issue(s);
-    const int32_t whole = p.K / kStepK;
-    for (int32_t step = 0; step < whole; ++step) {
-        if (step + STAGES - 2 < steps)
-            wait_stage<(STAGES - 2) * kLoads>();
-        else
-            wait_stage<0>();
-        if (step + STAGES - 1 < steps)
-            issue(step + STAGES - 1);
-        compute(step, true);
+    for (int s = 0; s < STAGES; ++s)
+        issue();
+    if (ahead == STAGES)                                      // the first stage only
+        wait_loads<(STAGES - 1) * kLoads>();
+    else
+        wait_loads<0>();
+    ahead -= 1;
+    if (ragged && steps == 1 && behind) {
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i)
+            *reinterpret_cast<i32x4*>(s_stage + (i * kWaves + wave) * 1024 + 16 * lane) =
+                i32x4{0, 0, 0, 0};
     }
-    if (whole < steps) {
-        wait_stage<0>();
-        compute(whole, false);
-    }
+    wait_workgroup();
+    for (int32_t tile = first; tile < last; tile += stride) {
+        const Tile t = tile_at<BM, kGroup>(p, s_prefix, tile);
+        int32_t src[MF];
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int32_t r = t.row0 + min((wm * MF + m) * 32 + r32, t.rows - 1);
+            src[m] = p.row_token ? p.row_token[r] : r;
+        }
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[m][f][i] = 0;
+        read(0, 0);
+        for (int32_t step = 0; step < steps - 1; ++step) {
+            read(1, 1);
+            multiply(0);
+            read(0, 2);
+            multiply(1);
+            read(1, 3);
+            multiply(0);
+            const int next = after(at);
+            landed(next, ragged && step == steps - 2);
+            wait_workgroup();                                 // and this stage is read
+            --ahead;
+            issue();
+            at = next;
+            read(0, 0);
+            multiply(1);
+        }
+        float sa[MF];
+        uint32_t rows[MF];                                    // a bit for each row to be written
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const bool ok = (uint32_t)src[m] < (uint32_t)p.a_rows &&
+                            (wm * MF + m) * 32 + r32 < t.rows;
+            sa[m] = p.a_scale[ok ? src[m] : 0];
+            rows[m] = (uint32_t)__ballot(ok);
+        }
+        read(1, 1);
+        multiply(0);
+        read(0, 2);
+        multiply(1);
+        read(1, 3);
+        multiply(0);
+        multiply(1);
+        const int next = after(at);
+        if (ahead > 0)
+            landed(next, ragged && steps == 1);
+        wait_workgroup();
 
-    // lane l has row l % 32 of a fragment and its channels 8 (i / 4) + 4 (l / 32) + i % 4
+        // Results: the stage just read is free, 8 KiB of it for each wavefront. Two fragments at a
+        // time go through it as fp32, 32 rows of 64 channels with piece c of row r in slot
+        // c ^ (r % 16), and come back as 8 consecutive channels a lane for 16-byte stores. (Stored
+        // straight from the accumulators, two bytes a store, they took as long as half the loop.)
+        int8_t* mine = s_stage + at + wave * 8192;
+        const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
+        constexpr int kLanes = SWIGLU ? 4 : 8;                // lanes of a row
+        const int col = 8 * (lane % kLanes);
+        const bool wide = p.N % 8 == 0 && (uintptr_t)p.out % 16 == 0;
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-        const int32_t at = (wm * MF + m) * 32 + r32;
-        if (at >= tile.rows)
-            continue;
-        const int32_t r = tile.row0 + at;
-        const int32_t src = p.row_token ? p.row_token[r] : r;
-        if ((uint32_t)src >= (uint32_t)p.a_rows)
-            continue;
-        const float sa = p.a_scale[src];
-        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N;
+        for (int f = 0; f < NF; f += 2) {
+            const int32_t n = n0 + (SWIGLU ? (wn * NF + f) * 16 : (wn * NF + f) * 32) + col;
+            const float* sw = p.w_scale + (int64_t)t.e * n_w;
+            float s0[8], s1[8];
 #pragma unroll
-        for (int f = 0; f < NF; f += SWIGLU ? 2 : 1) {
+            for (int i = 0; i < 8; ++i) {
+                const int32_t c = min(n + i, p.N - 1);
+                s0[i] = sw[c];
+                s1[i] = SWIGLU ? sw[p.N + c] : 0.0f;
+            }
 #pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-                const int32_t c = (wn * NF + f) * 32;
-                const int32_t n = n0 + (SWIGLU ? c / 2 : c) + 8 * i4 + 4 * half;
-                const int32_t left = p.N - n;
-                if (left <= 0)
-                    continue;
-                const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
-                float v[4];
+            for (int m = 0; m < MF; ++m) {
+                asm volatile("" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int o = i < left ? i : 0;
-                    v[i] = (float)acc[m][f][4 * i4 + i] * sa * sw[o];
-                    if (SWIGLU)
-                        v[i] = swiglu(v[i], (float)acc[m][f + (SWIGLU ? 1 : 0)][4 * i4 + i] * sa *
-                                                sw[p.N + o]);
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {             // channels 8 i + 4 half of fragment g
+                        f32x4 v;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            v[c] = (float)acc[m][f + g][4 * i + c] * sa[m];
+                        *reinterpret_cast<f32x4*>(
+                            mine + r32 * 256 + 16 * ((8 * g + 2 * i + half) ^ (r32 & 15))) = v;
+                    }
+                asm volatile("" ::: "memory");                // LDS serves a wavefront in order
+#pragma unroll
+                for (int pass = 0; pass < kLanes / 2; ++pass) {
+                    const int r = pass * (64 / kLanes) + lane / kLanes;
+                    const auto get = [&](int c) {
+                        return *reinterpret_cast<const f32x4*>(mine + r * 256 +
+                                                               16 * (c ^ (r & 15)));
+                    };
+                    float v[8];
+                    const int c0 = 2 * (lane % kLanes);
+                    const f32x4 x0 = get(c0), x1 = get(c0 + 1);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = (i < 4 ? x0[i] : x1[i - 4]) * s0[i];
+                    if (SWIGLU) {
+                        const f32x4 u0 = get(8 + c0), u1 = get(9 + c0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = swiglu(v[i], (i < 4 ? u0[i] : u1[i - 4]) * s1[i]);
+                    }
+                    if (!(rows[m] >> r & 1))
+                        continue;
+                    OUT* out = static_cast<OUT*>(p.out) +
+                               (int64_t)(t.row0 + (wm * MF + m) * 32 + r) * p.N + n;
+                    if (wide) {
+                        if (n < p.N)
+                            store8(out, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < p.N)
+                                out[i] = (OUT)v[i];
+                    }
                 }
-                store4(out + n, left, v);
             }
         }
+        wait_workgroup();
+        if (ahead > 0) {
+            --ahead;
+            issue();
+        }
+        at = next;
     }
 }
 
@@ -635,9 +858,10 @@ bool launch_tile(MatmulArgs p, hipStream_t stream)
 {
     constexpr int kThreads = 64 * WM * WN, kLds = STAGES * (BM + BN) * kStepK;
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? BN / 2 : BN);
-    const int64_t blocks = div_up(most_tiles(p, BM) * p.n_blocks, kXcds) * kXcds;
-    if (blocks * kThreads > INT32_MAX)
+    const int64_t tiles = most_tiles(p, BM) * p.n_blocks;
+    if (tiles > INT32_MAX / 2)
         return false;
+    const int64_t blocks = tiles < kCus ? div_up(tiles, kXcds) * kXcds : kCus;
     const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, SWIGLU, OUT>;
     if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
                                             hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -654,8 +878,8 @@ bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
     if (rows < 32)
         return launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
     if (rows < 160)
-        return launch_tile<128, 256, 2, 4, 3, SWIGLU, OUT>(p, stream);
-    return launch_tile<256, 256, 2, 4, 2, SWIGLU, OUT>(p, stream);
+        return launch_tile<128, 256, 2, 2, 3, SWIGLU, OUT>(p, stream);
+    return launch_tile<256, 256, 4, 2, 2, SWIGLU, OUT>(p, stream);
 }
 
 moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
