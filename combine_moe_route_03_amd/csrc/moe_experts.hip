@@ -287,9 +287,17 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p)
     return tile;
 }
 
+// gate / (1 + exp(-gate)) * up, with exp(x) = 2^(x log2 e): the product's rounding, |gate| 2^-24
+// of the result, is added back to first order; v_exp_f32 and v_rcp_f32 are good to one ulp. Beyond
+// 2^126 (the quotient is below 2^-119 then) exp goes without, so that infinity stays one.
 __device__ __forceinline__ float swiglu(float gate, float up)
 {
-    return gate / (1.0f + expf(-gate)) * up;
+    constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
+    const float t = gate * hi;
+    const float rest = __builtin_fmaf(gate, hi, -t) + gate * lo;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float s = 1.0f + (t > 126.0f ? e : __builtin_fmaf(e, rest * 0.693147182f, e));
+    return gate * __builtin_amdgcn_rcpf(s) * up;
 }
 
 __device__ __forceinline__ void store4(float* p, int n, const float v[4])
@@ -458,21 +466,22 @@ __device__ __forceinline__ void wait_workgroup()
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ void store8(float* p, const float v[8])
+// 16 bytes to `buffer` at voff, dropped where that is out of its range. Not for the caches: the
+// next kernel reads the results from their start, and only the last ones would still be there.
+__device__ __forceinline__ void store_buffer(u32x4 v, __amdgpu_buffer_rsrc_t buffer, uint32_t voff)
 {
-    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_amdgcn_raw_buffer_store_b128(v, buffer, voff, 0, 2 /* nt */);
 }
 
-__device__ __forceinline__ void store8(__bf16* p, const float v[8])
-{
-    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-    bf16x8 b;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        b[i] = (__bf16)v[i];
-    *reinterpret_cast<bf16x8*>(p) = b;
-}
+// Four results as they are kept in memory.
+template <typename OUT>
+struct Four {
+    typedef f32x4 type;
+};
+template <>
+struct Four<__bf16> {
+    typedef bf16x4 type;
+};
 
 // Exclusive prefix of the experts' row tiles into prefix[0 .. E] (every thread calls), and their
 // total. Offsets are clamped into [0, R], so no value of theirs leads outside the rows.
@@ -552,12 +561,12 @@ __device__ __forceinline__ Tile tile_at(const MatmulArgs& p, const int32_t* pref
     const int32_t m = group * GROUP + in % side;
     int32_t lo;
     const int32_t n = expert_rows(p, e, &lo);
-    t.row0 = lo + m * BM;
-    t.rows = min(BM, n - m * BM);
+    t.row0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
+    t.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
     return t;
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, typename OUT>
+template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
 {
     constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -568,9 +577,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     constexpr int kGroup = 4;
     static_assert(MF * WM * 32 == BM && NF * WN * 32 == BN, "tile");
     static_assert(kLoadsA * 8 * kWaves == BM && kLoadsW * 8 * kWaves == BN, "loads");
-    static_assert(NF % 2 == 0 && kWaves * 8192 <= kStage && STAGES >= 2, "pairs of fragments");
+    static_assert(NF % 2 == 0 && STAGES >= 2, "pairs of fragments");
+    // results of a wavefront: fragments side by side, and the 2 KiB units they are stored in
+    constexpr int kOutF = SWIGLU ? NF / 2 : NF, kUnitF = kOutF < 2 ? 1 : 2;
+    constexpr int kUnitRow = kUnitF * 32 * (int)sizeof(OUT), kUnitRows = 2048 / kUnitRow < 32 ? 2048 / kUnitRow : 32;
+    constexpr int kUnitStores = kUnitRows * kUnitRow / 1024;
+    constexpr int kStores = MF * (32 / kUnitRows) * (kOutF / kUnitF) * kUnitStores;
+    static_assert(kOutF % kUnitF == 0 && kUnitStores >= 1 && BM <= kThreads, "results");
+    static_assert((STAGES - 2) * kLoads + kStores <= 63, "vmcnt has six bits");
     extern __shared__ __attribute__((aligned(1024))) int8_t s_stage[];
+    __shared__ __attribute__((aligned(16))) int8_t s_unit[kWaves][2048];
     __shared__ int32_t s_prefix[MOE_MAX_EXPERTS + 1];
+    __shared__ __attribute__((aligned(16))) float s_ws[BN];
+    __shared__ float s_as[BM];
+    __shared__ uint32_t s_ok[BM / 32];                        // a bit for each row to be written
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
@@ -594,6 +614,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     int32_t load_tile = first, load_step = 0;
     uint32_t load_to = lds0 + wave * 1024;
     int32_t ahead = 0;                                        // stages loaded and not yet begun
+    int32_t older = 0;                                        // of these, before the last stores
     const auto aim = [&]() {
         const Tile t = tile_at<BM, kGroup>(p, s_prefix, load_tile);
         abuf = p.row_token ? buffer_of(p.a, (uint32_t)((int64_t)p.a_rows * p.K))
@@ -654,7 +675,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         slot[q] = r32 * kStepK + 16 * ((2 * q + half) ^ (r32 & 7));
     int at = 0;                                               // the stage that is multiplied
     i32x4 wv[2][NF], av[2][MF];
-    const auto read = [&](int set, int q) {
+    const auto read = [&](int set, int q) {                   // quarter q of the stage
         const int8_t* sw = s_stage + at + (BM + wn * NF * 32) * kStepK + slot[q];
         const int8_t* sa = s_stage + at + wm * MF * 32 * kStepK + slot[q];
 #pragma unroll
@@ -664,20 +685,45 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         for (int m = 0; m < MF; ++m)
             av[set][m] = *reinterpret_cast<const i32x4*>(sa + m * 32 * kStepK);
     };
-    const auto multiply = [&](int set) {
+    // Multiplies operand set `cur` while quarter q goes into the other set. PIN: the reads stay
+    // spread out among the products, where the compiler would group them.
+    const auto multiply = [&](int cur, int q) {
+        constexpr int kProducts = MF * NF, kReads = MF + NF;
+        const int8_t* sw = s_stage + at + (BM + wn * NF * 32) * kStepK + slot[q < 0 ? 0 : q];
+        const int8_t* sa = s_stage + at + wm * MF * 32 * kStepK + slot[q < 0 ? 0 : q];
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
+        for (int i = 0; i < kProducts; ++i) {
+            const int m = i / NF, f = m & 1 ? NF - 1 - i % NF : i % NF;
+            acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[cur][f], av[cur][m], acc[m][f],
+                                                              0, 0, 0);
+            if (PIN)
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                acc[m][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][f], av[set][m],
-                                                                  acc[m][f], 0, 0, 0);
+            for (int j = 0; j < kReads; ++j) {
+                if (q < 0 || j * kProducts / kReads != i)
+                    continue;
+                if (j == 0)
+                    av[1 - cur][0] = *reinterpret_cast<const i32x4*>(sa);
+                else if (j <= NF)
+                    wv[1 - cur][j - 1] =
+                        *reinterpret_cast<const i32x4*>(sw + (j - 1) * 32 * kStepK);
+                else
+                    av[1 - cur][j - NF] =
+                        *reinterpret_cast<const i32x4*>(sa + (j - NF) * 32 * kStepK);
+                if (PIN)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     };
     // this wavefront's loads of the next stage have landed; `partial`: it is a ragged last step
     const auto landed = [&](int32_t next, bool partial) {
-        if (ahead >= STAGES - 1)
-            wait_loads<(STAGES - 2) * kLoads>();
-        else
+        if (ahead < STAGES - 1)
             wait_loads<0>();
+        else if (older > 0)                                   // the stores may still be on their way
+            wait_loads<(STAGES - 2) * kLoads + kStores>();
+        else
+            wait_loads<(STAGES - 2) * kLoads>();
+        --older;
         if (partial && behind) {
 #pragma unroll
             for (int i = 0; i < kLoadsA; ++i)
@@ -704,12 +750,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     }
     wait_workgroup();
     for (int32_t tile = first; tile < last; tile += stride) {
+        if (steps == 1)                                       // no wait in the loop keeps the
+            wait_workgroup();                                 // tiles' scales apart
         const Tile t = tile_at<BM, kGroup>(p, s_prefix, tile);
-        int32_t src[MF];
+        // scales: a thread's row of the tile, and its channels, put into LDS at the tile's end
+        const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
+        const bool mine = tid < t.rows;
+        const int32_t row = t.row0 + (mine ? tid : 0);
+        const int32_t src = p.row_token ? p.row_token[row] : row;
+        float ws[(BN + kThreads - 1) / kThreads];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int32_t r = t.row0 + min((wm * MF + m) * 32 + r32, t.rows - 1);
-            src[m] = p.row_token ? p.row_token[r] : r;
+        for (int i = 0; i < (BN + kThreads - 1) / kThreads; ++i) {
+            const int32_t c = min(i * kThreads + tid, BN - 1);
+            const int32_t n = min(SWIGLU ? n0 + c / 64 * 32 + c % 32 : n0 + c, p.N - 1);
+            ws[i] = p.w_scale[(int64_t)t.e * n_w + n + (SWIGLU && (c & 32) ? p.N : 0)];
         }
 #pragma unroll
         for (int m = 0; m < MF; ++m)
@@ -720,118 +774,123 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
                     acc[m][f][i] = 0;
         read(0, 0);
         for (int32_t step = 0; step < steps - 1; ++step) {
-            read(1, 1);
-            multiply(0);
-            read(0, 2);
-            multiply(1);
-            read(1, 3);
-            multiply(0);
+            multiply(0, 1);
+            multiply(1, 2);
+            multiply(0, 3);
             const int next = after(at);
             landed(next, ragged && step == steps - 2);
             wait_workgroup();                                 // and this stage is read
             --ahead;
             issue();
             at = next;
-            read(0, 0);
-            multiply(1);
+            multiply(1, 0);
         }
-        float sa[MF];
-        uint32_t rows[MF];                                    // a bit for each row to be written
+        const bool ok = mine && (uint32_t)src < (uint32_t)p.a_rows;
+        const float as = p.a_scale[ok ? src : 0];
+        multiply(0, 1);
+        multiply(1, 2);
+        multiply(0, 3);
+        multiply(1, -1);
+        if (tid < BM)
+            s_as[tid] = as;
+        const uint64_t oks = __ballot(ok);
+        if (lane < 2 && wave * 2 + lane < BM / 32)
+            s_ok[wave * 2 + lane] = (uint32_t)(oks >> (32 * lane));
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const bool ok = (uint32_t)src[m] < (uint32_t)p.a_rows &&
-                            (wm * MF + m) * 32 + r32 < t.rows;
-            sa[m] = p.a_scale[ok ? src[m] : 0];
-            rows[m] = (uint32_t)__ballot(ok);
-        }
-        read(1, 1);
-        multiply(0);
-        read(0, 2);
-        multiply(1);
-        read(1, 3);
-        multiply(0);
-        multiply(1);
+        for (int i = 0; i < (BN + kThreads - 1) / kThreads; ++i)
+            if (i * kThreads + tid < BN)
+                s_ws[i * kThreads + tid] = ws[i];
         const int next = after(at);
         if (ahead > 0)
             landed(next, ragged && steps == 1);
         wait_workgroup();
+        older = 0;
+        if (ahead > 0) {
+            --ahead;
+            issue();
+            older = ahead;
+        }
+        at = next;
 
-        // Results: the stage just read is free, 8 KiB of it for each wavefront. Two fragments at a
-        // time go through it as fp32, 32 rows of 64 channels with piece c of row r in slot
-        // c ^ (r % 16), and come back as 8 consecutive channels a lane for 16-byte stores. (Stored
-        // straight from the accumulators, two bytes a store, they took as long as half the loop.)
-        int8_t* mine = s_stage + at + wave * 8192;
-        const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
-        constexpr int kLanes = SWIGLU ? 4 : 8;                // lanes of a row
-        const int col = 8 * (lane % kLanes);
-        const bool wide = p.N % 8 == 0 && (uintptr_t)p.out % 16 == 0;
+        // Results, while the next tile's first stages are on their way: the lane's fp32 values are
+        // rounded, go through 2 KiB of LDS of the wavefront's own, and come back as rows of 128
+        // bytes (bf16) for 16-byte stores; 16-byte piece c of row r lies in slot c ^ (r % 8).
+        // Stores of whole rows count the same for every wavefront, so that the loads before them
+        // can be waited for without them. (Stored from the accumulators two bytes at a time, the
+        // results of 8192^3 took 150 of 621 us; with the stores waited for at once, 50 of 470.)
+        constexpr int kPieces = kUnitRow / 16;
+        const bool wide = p.N % (16 / (int)sizeof(OUT)) == 0 && (uintptr_t)p.out % 16 == 0 &&
+                          p.N <= (1 << 20);
+        OUT* base = static_cast<OUT*>(p.out) + (int64_t)t.row0 * p.N;
+        const __amdgpu_buffer_rsrc_t obuf = __builtin_amdgcn_make_buffer_rsrc(
+            base, 0, (int32_t)((uint32_t)t.rows * (uint32_t)p.N * (uint32_t)sizeof(OUT)), 0x00020000);
+        int8_t* unit = s_unit[wave];
+        if (!wide)
+            older = 0;
 #pragma unroll
-        for (int f = 0; f < NF; f += 2) {
-            const int32_t n = n0 + (SWIGLU ? (wn * NF + f) * 16 : (wn * NF + f) * 32) + col;
-            const float* sw = p.w_scale + (int64_t)t.e * n_w;
-            float s0[8], s1[8];
+        for (int m = 0; m < MF; ++m) {
+            const float sa = s_as[(wm * MF + m) * 32 + r32];
+            const uint32_t rows = s_ok[wm * MF + m];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int32_t c = min(n + i, p.N - 1);
-                s0[i] = sw[c];
-                s1[i] = SWIGLU ? sw[p.N + c] : 0.0f;
-            }
+            for (int u = 0; u < kOutF; u += kUnitF) {
+                typename Four<OUT>::type v[kUnitF][4];        // channels 8 i + 4 half
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                asm volatile("" ::: "memory");
+                for (int g = 0; g < kUnitF; ++g)
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                    for (int i = 0; i < 4; ++i) {
+                        const int f = SWIGLU ? 2 * (u + g) : u + g;
+                        const float* sw = s_ws + (wn * NF + f) * 32 + 8 * i + 4 * half;
+                        const f32x4 s0 = *reinterpret_cast<const f32x4*>(sw);
+                        const f32x4 s1 = *reinterpret_cast<const f32x4*>(SWIGLU ? sw + 32 : sw);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {             // channels 8 i + 4 half of fragment g
-                        f32x4 v;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            v[c] = (float)acc[m][f + g][4 * i + c] * sa[m];
-                        *reinterpret_cast<f32x4*>(
-                            mine + r32 * 256 + 16 * ((8 * g + 2 * i + half) ^ (r32 & 15))) = v;
+                        for (int c = 0; c < 4; ++c) {
+                            float y = (float)acc[m][f][4 * i + c] * sa * s0[c];
+                            if (SWIGLU)
+                                y = swiglu(y, (float)acc[m][f + SWIGLU][4 * i + c] * sa * s1[c]);
+                            v[g][i][c] = (OUT)y;
+                        }
                     }
-                asm volatile("" ::: "memory");                // LDS serves a wavefront in order
+#pragma unroll 1
+                for (int phase = 0; phase < 32 / kUnitRows; ++phase) {
+                    asm volatile("" ::: "memory");            // LDS serves a wavefront in order
+                    if (r32 / kUnitRows == phase) {
+                        const int r = r32 % kUnitRows;
 #pragma unroll
-                for (int pass = 0; pass < kLanes / 2; ++pass) {
-                    const int r = pass * (64 / kLanes) + lane / kLanes;
-                    const auto get = [&](int c) {
-                        return *reinterpret_cast<const f32x4*>(mine + r * 256 +
-                                                               16 * (c ^ (r & 15)));
-                    };
-                    float v[8];
-                    const int c0 = 2 * (lane % kLanes);
-                    const f32x4 x0 = get(c0), x1 = get(c0 + 1);
+                        for (int g = 0; g < kUnitF; ++g)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = (i < 4 ? x0[i] : x1[i - 4]) * s0[i];
-                    if (SWIGLU) {
-                        const f32x4 u0 = get(8 + c0), u1 = get(9 + c0);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[i] = swiglu(v[i], (i < 4 ? u0[i] : u1[i - 4]) * s1[i]);
+                            for (int i = 0; i < 4; ++i) {
+                                const int byte = (32 * g + 8 * i + 4 * half) * (int)sizeof(OUT);
+                                *reinterpret_cast<typename Four<OUT>::type*>(
+                                    unit + r * kUnitRow +
+                                    ((byte / 16 ^ (r & (kPieces - 1) & 7)) * 16) + byte % 16) =
+                                    v[g][i];
+                            }
                     }
-                    if (!(rows[m] >> r & 1))
-                        continue;
-                    OUT* out = static_cast<OUT*>(p.out) +
-                               (int64_t)(t.row0 + (wm * MF + m) * 32 + r) * p.N + n;
-                    if (wide) {
-                        if (n < p.N)
-                            store8(out, v);
-                    } else {
+                    asm volatile("" ::: "memory");
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n + i < p.N)
-                                out[i] = (OUT)v[i];
+                    for (int s = 0; s < kUnitStores; ++s) {
+                        const int r = s * (kUnitRows / kUnitStores) + lane / kPieces;
+                        const int c = lane % kPieces;
+                        const int rr = phase * kUnitRows + r;
+                        const u32x4 out = *reinterpret_cast<const u32x4*>(
+                            unit + r * kUnitRow + (c ^ (r & (kPieces - 1) & 7)) * 16);
+                        const int32_t n = n0 + (wn * kOutF + u) * 32 + c * (16 / (int)sizeof(OUT));
+                        const int32_t tr = (wm * MF + m) * 32 + rr;
+                        const bool write = (rows >> rr & 1) && n < p.N;
+                        if (wide) {
+                            store_buffer(out, obuf, write ? (uint32_t)(tr * p.N + n) * (uint32_t)sizeof(OUT)
+                                                        : 0xFFFFFFF0u);
+                        } else if (write) {
+                            const OUT* x = reinterpret_cast<const OUT*>(
+                                unit + r * kUnitRow + (c ^ (r & (kPieces - 1) & 7)) * 16);
+                            const int left = min(16 / (int)sizeof(OUT), p.N - n);
+                            for (int i = 0; i < left; ++i)
+                                base[(int64_t)tr * p.N + n + i] = x[i];
+                        }
                     }
                 }
             }
         }
-        wait_workgroup();
-        if (ahead > 0) {
-            --ahead;
-            issue();
-        }
-        at = next;
     }
 }
 
@@ -853,7 +912,7 @@ bool launch_few(MatmulArgs p, hipStream_t stream)
     return true;
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, typename OUT>
+template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool SWIGLU, typename OUT>
 bool launch_tile(MatmulArgs p, hipStream_t stream)
 {
     constexpr int kThreads = 64 * WM * WN, kLds = STAGES * (BM + BN) * kStepK;
@@ -862,7 +921,7 @@ bool launch_tile(MatmulArgs p, hipStream_t stream)
     if (tiles > INT32_MAX / 2)
         return false;
     const int64_t blocks = tiles < kCus ? div_up(tiles, kXcds) * kXcds : kCus;
-    const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, SWIGLU, OUT>;
+    const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, PIN, SWIGLU, OUT>;
     if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
                                             hipFuncAttributeMaxDynamicSharedMemorySize,
                                             kLds) != hipSuccess)
@@ -878,8 +937,8 @@ bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
     if (rows < 32)
         return launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
     if (rows < 160)
-        return launch_tile<128, 256, 2, 2, 3, SWIGLU, OUT>(p, stream);
-    return launch_tile<256, 256, 4, 2, 2, SWIGLU, OUT>(p, stream);
+        return launch_tile<128, 256, 2, 2, 3, false, SWIGLU, OUT>(p, stream);
+    return launch_tile<256, 256, 4, 2, 2, true, SWIGLU, OUT>(p, stream);
 }
 
 moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
