@@ -195,6 +195,7 @@ struct MatmulArgs {
     void* out;
     int32_t a_rows, R, E, N, K;
     int32_t n_blocks;          // workgroups side by side over the channels
+    double inv_blocks;         // 1 / n_blocks
 };
 
 // Rows [row0, row0 + rows) of expert e, channel block n; rows = 0: nothing to do.
@@ -202,89 +203,53 @@ struct Tile {
     int32_t e, row0, rows, n;
 };
 
-// The tile of workgroup blockIdx.x (every thread calls): tiles of BM rows by p.n_blocks channel
-// blocks, expert by expert. Each thread adds up the row tiles of its share of the experts, a scan
-// over the workgroup gives the total and finds the thread whose share holds the workgroup's tile.
-// The host only knows a bound of the total, so workgroups beyond it have nothing to do. Offsets are
-// clamped into [0, R], so no value of theirs leads outside the rows.
-//   Workgroup b runs on XCD b % 8: an XCD takes a run of consecutive tiles, GROUP row tiles by all
-// channel blocks at a time (row tiles fastest), so that the workgroups that run together on it
-// share weights and rows in its L2.
-template <int THREADS, int BM, int GROUP>
-__device__ __forceinline__ Tile find_tile(const MatmulArgs& p)
+// Rows of expert e and the first of them. Offsets are clamped into [0, R], so no value of theirs
+// leads outside the rows.
+__device__ __forceinline__ int32_t expert_rows(const MatmulArgs& p, int32_t e, int32_t* lo)
 {
-    __shared__ int32_t s_wave[THREADS / 64];
-    __shared__ int32_t s_found[3];
-    const int tid = threadIdx.x;
-    const int per = (p.E + THREADS - 1) / THREADS;
-    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
-    const auto rows_of = [&](int e, int32_t* lo) {
-        if (!p.offsets) {
-            *lo = 0;
-            return p.R;
-        }
-        *lo = min(max(p.offsets[e], 0), p.R);
-        return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
-    };
-    const auto tiles_of = [](int32_t n) { return n / BM + (n % BM != 0); };
-    int32_t mine = 0;
-    for (int e = e0; e < e1; ++e) {
-        int32_t lo;
-        mine += tiles_of(rows_of(e, &lo));
+    if (!p.offsets) {
+        *lo = 0;
+        return p.R;
     }
+    *lo = min(max(p.offsets[e], 0), p.R);
+    return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
+}
+
+// Row tile `index` of all experts' tiles of BM rows, found by each wavefront for itself: a lane
+// adds up the tiles of its share of the experts, a scan over the lanes finds the share that holds
+// the index.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t index)
+{
+    const int lane = threadIdx.x & 63;
+    const int per = (p.E + 63) / 64;
+    const int e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
+    int32_t mine = 0, lo = 0;
+    for (int e = e0; e < e1; ++e)
+        mine += (expert_rows(p, e, &lo) + BM - 1) / BM;
     int32_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int32_t o = __shfl_up(upto, d);
-        if ((tid & 63) >= d)
+        if (lane >= d)
             upto += o;
     }
-    if ((tid & 63) == 63)
-        s_wave[tid >> 6] = upto;
-    __syncthreads();
-    int32_t total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-        if (w < (tid >> 6))
-            upto += s_wave[w];
-        total += s_wave[w];
+    const int32_t before = upto - mine;
+    const uint64_t holds = __ballot(before <= index && index < upto);
+    if (holds == 0)
+        return Tile{0, 0, 0, 0};
+    const int at = __ffsll((unsigned long long)holds) - 1;
+    int32_t e = __builtin_amdgcn_readlane(e0, at);
+    int32_t left = index - __builtin_amdgcn_readlane(before, at), n;
+    for (;; ++e) {
+        n = expert_rows(p, e, &lo);
+        const int32_t tiles = (n + BM - 1) / BM;
+        if (left < tiles)
+            break;
+        left -= tiles;
     }
-    const int64_t all = (int64_t)total * p.n_blocks;
-    const int64_t share = (all + kXcds - 1) / kXcds;
-    const int64_t at = (int64_t)(blockIdx.x % kXcds) * share + blockIdx.x / kXcds;
-    if (blockIdx.x / kXcds >= share || at >= all)
-        return Tile{0, 0, 0, 0};                              // the same for the whole workgroup
-    const int64_t index = at / p.n_blocks;                    // a row tile of the same expert
-    int32_t before = upto - mine;
-    if (before <= index && index < upto) {
-        for (int e = e0; e < e1; ++e) {
-            int32_t lo;
-            const int32_t tiles = tiles_of(rows_of(e, &lo));
-            if (index < before + tiles) {
-                s_found[0] = e;
-                s_found[1] = before;
-                s_found[2] = tiles;
-                break;
-            }
-            before += tiles;
-        }
-    }
-    __syncthreads();
-    Tile tile;
-    tile.e = __builtin_amdgcn_readfirstlane(s_found[0]);
-    before = __builtin_amdgcn_readfirstlane(s_found[1]);
-    const int32_t tiles = __builtin_amdgcn_readfirstlane(s_found[2]);
-    const int64_t local = at - (int64_t)before * p.n_blocks;
-    const int32_t group = (int32_t)(local / ((int64_t)GROUP * p.n_blocks));
-    const int32_t in = (int32_t)(local - (int64_t)group * GROUP * p.n_blocks);
-    const int32_t side = min(GROUP, tiles - group * GROUP);
-    tile.n = in / side;
-    const int32_t m = group * GROUP + in % side;
-    int32_t lo;
-    const int32_t n = rows_of(tile.e, &lo);
-    tile.row0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
-    tile.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
-    return tile;
+    return Tile{e, __builtin_amdgcn_readfirstlane(lo + left * BM),
+                __builtin_amdgcn_readfirstlane(min(BM, n - left * BM)), 0};
 }
 
 // gate / (1 + exp(-gate)) * up, with exp(x) = 2^(x log2 e): the product's rounding, |gate| 2^-24
@@ -300,19 +265,15 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     return gate * __builtin_amdgcn_rcpf(s) * up;
 }
 
-__device__ __forceinline__ void store4(float* p, int n, const float v[4])
-{
-    for (int i = 0; i < 4; ++i)
-        if (i < n)
-            p[i] = v[i];
-}
-
-__device__ __forceinline__ void store4(__bf16* p, int n, const float v[4])
-{
-    for (int i = 0; i < 4; ++i)
-        if (i < n)
-            p[i] = (__bf16)v[i];
-}
+// Four results as they are kept in memory.
+template <typename OUT>
+struct Four {
+    typedef f32x4 type;
+};
+template <>
+struct Four<__bf16> {
+    typedef bf16x4 type;
+};
 
 // Few rows an expert: bound by reading the weights, each once. A workgroup takes up to 16 MF rows
 // of one expert and 16 NF channels; its wavefronts share the K axis out by 128-byte pieces, read
@@ -320,15 +281,16 @@ __device__ __forceinline__ void store4(__bf16* p, int n, const float v[4])
 // any order gives the same). v_mfma_i32_16x16x64_i8 with the weights as the left operand: lane l
 // gives channel l % 16 and 16 bytes of K at 16 (l / 16), and gets row l % 16 with channels
 // 4 (l / 16) + i, so that its four results lie side by side in memory.
-template <int MF, int NF, int WAVES, bool SWIGLU, typename OUT>
+template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
 {
-    __shared__ i32x4 s_acc[WAVES][64];
+    constexpr int kFrags = MF * NF;
+    __shared__ i32x4 s_acc[WAVES][kFrags][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Tile tile = find_tile<64 * WAVES, 16 * MF, 4>(p);
+    const int32_t nb = blockIdx.x % p.n_blocks;
+    const Tile tile = find_tile<16 * MF>(p, blockIdx.x / p.n_blocks);
     if (tile.rows == 0)
         return;
-    const int nb = tile.n;
     const int r16 = lane & 15, kq = lane >> 4;
     const int32_t n_w = SWIGLU ? 2 * p.N : p.N;               // channels of w
     const int8_t* we = p.w + (int64_t)tile.e * n_w * p.K;
@@ -358,69 +320,79 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
         for (int f = 0; f < NF; ++f)
             acc[m][f] = i32x4{0, 0, 0, 0};
 
-    for (int32_t k0 = wave * 128; k0 < p.K; k0 += WAVES * 128) {
+    for (int32_t k0 = wave * 128; k0 < p.K; k0 += U * WAVES * 128) {
+        i32x4 wv[2 * U][NF], av[2 * U][MF];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int32_t at = k0 + 64 * h + 16 * kq;
+        for (int h = 0; h < 2 * U; ++h) {
+            const int32_t at = k0 + h / 2 * WAVES * 128 + 64 * (h % 2) + 16 * kq;
             const bool in = at < p.K;                         // K is a multiple of 16
-            i32x4 wv[NF], av[MF];
+            const int32_t from = in ? at : 0;
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                wv[f] = in ? *reinterpret_cast<const i32x4*>(wp[f] + at) : i32x4{0, 0, 0, 0};
+                wv[h][f] = *reinterpret_cast<const i32x4*>(wp[f] + from);
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
-                av[m] = in ? *reinterpret_cast<const i32x4*>(ap[m] + at) : i32x4{0, 0, 0, 0};
+            for (int m = 0; m < MF; ++m) {
+                av[h][m] = *reinterpret_cast<const i32x4*>(ap[m] + from);
+                av[h][m] = in ? av[h][m] : i32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2 * U; ++h)
 #pragma unroll
             for (int m = 0; m < MF; ++m)
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
-                    acc[m][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[f], av[m], acc[m][f], 0,
-                                                                      0, 0);
-        }
+                    acc[m][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[h][f], av[h][m],
+                                                                      acc[m][f], 0, 0, 0);
     }
-    // join the wavefronts, fragment by fragment
+    // the wavefronts' sums of each fragment (with SwiGLU of each pair) are joined by one of them
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            __syncthreads();
-            s_acc[wave][lane] = acc[m][f];
-            __syncthreads();
-            if (wave == 0) {
+        for (int f = 0; f < NF; ++f)
+            s_acc[wave][m * NF + f][lane] = acc[m][f];
+    __syncthreads();
+    constexpr int kStep = SWIGLU ? 2 : 1;
+    for (int i = wave * kStep; i < kFrags; i += WAVES * kStep) {
+        const int m = i / NF, f = i % NF;
+        i32x4 sum[2];
 #pragma unroll
-                for (int w = 1; w < WAVES; ++w)
-                    acc[m][f] += s_acc[w][lane];
-            }
+        for (int g = 0; g < kStep; ++g) {
+            sum[g] = s_acc[0][i + g][lane];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w)
+                sum[g] += s_acc[w][i + g][lane];
         }
-    if (wave != 0)
-        return;
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
         const int32_t at = 16 * m + r16;
-        if (at >= tile.rows)
-            continue;
-        const int32_t r = tile.row0 + at;
+        const int32_t r = tile.row0 + min(at, tile.rows - 1);
         const int32_t src = p.row_token ? p.row_token[r] : r;
-        if ((uint32_t)src >= (uint32_t)p.a_rows)
+        const int32_t n = n0 + (SWIGLU ? 8 : 16) * f + 4 * kq;
+        const int32_t left = p.N - n;
+        if (at >= tile.rows || (uint32_t)src >= (uint32_t)p.a_rows || left <= 0)
             continue;
         const float sa = p.a_scale[src];
-        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N;
+        const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
+        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N + n;
+        float v[4];
 #pragma unroll
-        for (int f = 0; f < NF; f += SWIGLU ? 2 : 1) {
-            const int32_t n = (SWIGLU ? n0 + 8 * f : n0 + 16 * f) + 4 * kq;
-            const int32_t left = p.N - n;
-            if (left <= 0)
-                continue;
-            const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
-            float v[4];
+        for (int c = 0; c < 4; ++c) {
+            const int o = c < left ? c : 0;
+            v[c] = (float)sum[0][c] * sa * sw[o];
+            if (SWIGLU)
+                v[c] = swiglu(v[c], (float)sum[kStep - 1][c] * sa * sw[p.N + o]);
+        }
+        typedef typename Four<OUT>::type four;
+        if (left >= 4 && (uintptr_t)out % sizeof(four) == 0) {
+            four x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int o = i < left ? i : 0;
-                v[i] = (float)acc[m][f][i] * sa * sw[o];
-                if (SWIGLU)
-                    v[i] = swiglu(v[i], (float)acc[m][f + (SWIGLU ? 1 : 0)][i] * sa * sw[p.N + o]);
-            }
-            store4(out + n, left, v);
+            for (int c = 0; c < 4; ++c)
+                x[c] = (OUT)v[c];
+            *reinterpret_cast<four*>(out) = x;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c < left)
+                    out[c] = (OUT)v[c];
         }
     }
 }
@@ -473,28 +445,8 @@ __device__ __forceinline__ void store_buffer(u32x4 v, __amdgpu_buffer_rsrc_t buf
     __builtin_amdgcn_raw_buffer_store_b128(v, buffer, voff, 0, 2 /* nt */);
 }
 
-// Four results as they are kept in memory.
-template <typename OUT>
-struct Four {
-    typedef f32x4 type;
-};
-template <>
-struct Four<__bf16> {
-    typedef bf16x4 type;
-};
-
 // Exclusive prefix of the experts' row tiles into prefix[0 .. E] (every thread calls), and their
-// total. Offsets are clamped into [0, R], so no value of theirs leads outside the rows.
-__device__ __forceinline__ int32_t expert_rows(const MatmulArgs& p, int32_t e, int32_t* lo)
-{
-    if (!p.offsets) {
-        *lo = 0;
-        return p.R;
-    }
-    *lo = min(max(p.offsets[e], 0), p.R);
-    return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
-}
-
+// total.
 template <int THREADS, int BM>
 __device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* prefix)
 {
@@ -538,12 +490,23 @@ __device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* pre
     return __builtin_amdgcn_readfirstlane(total);
 }
 
+// x / n of the same value in every lane, x >= 0, by inv = 1 / n in fp64: off by one at most.
+__device__ __forceinline__ int32_t quotient(int32_t x, int32_t n, double inv)
+{
+    int32_t q = __builtin_amdgcn_readfirstlane((int32_t)((double)x * inv));
+    const int32_t r = x - q * n;
+    q -= r < 0;
+    q += r >= n;
+    return q;
+}
+
 // Tile `at` of all: expert by expert, GROUP row tiles by all channel blocks at a time, row tiles
 // fastest, so that tiles that run together on an XCD share weights and rows in its L2.
 template <int BM, int GROUP>
 __device__ __forceinline__ Tile tile_at(const MatmulArgs& p, const int32_t* prefix, int32_t at)
 {
-    const int32_t index = at / p.n_blocks;
+    static_assert(GROUP == 4, "side is at most 4");
+    const int32_t index = quotient(at, p.n_blocks, p.inv_blocks);
     int32_t e = -1;
     for (int j = 0; j < p.E; j += 64) {
         const int i = j + (threadIdx.x & 63);
@@ -552,13 +515,13 @@ __device__ __forceinline__ Tile tile_at(const MatmulArgs& p, const int32_t* pref
     const int32_t before = __builtin_amdgcn_readfirstlane(prefix[e]);
     const int32_t tiles = __builtin_amdgcn_readfirstlane(prefix[e + 1]) - before;
     const int32_t local = at - before * p.n_blocks;
-    const int32_t group = local / (GROUP * p.n_blocks);
+    const int32_t group = quotient(local, GROUP * p.n_blocks, p.inv_blocks / GROUP);
     const int32_t in = local - group * GROUP * p.n_blocks;
     const int32_t side = min(GROUP, tiles - group * GROUP);
     Tile t;
     t.e = e;
-    t.n = in / side;
-    const int32_t m = group * GROUP + in % side;
+    t.n = side == 4 ? in >> 2 : side == 3 ? (int32_t)((uint32_t)in / 3u) : side == 2 ? in >> 1 : in;
+    const int32_t m = group * GROUP + in - t.n * side;
     int32_t lo;
     const int32_t n = expert_rows(p, e, &lo);
     t.row0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
@@ -578,19 +541,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     static_assert(MF * WM * 32 == BM && NF * WN * 32 == BN, "tile");
     static_assert(kLoadsA * 8 * kWaves == BM && kLoadsW * 8 * kWaves == BN, "loads");
     static_assert(NF % 2 == 0 && STAGES >= 2, "pairs of fragments");
-    // results of a wavefront: fragments side by side, and the 2 KiB units they are stored in
+    // results of a wavefront: fragments side by side, and the units they are stored in
+    constexpr int kUnit = 8192 / kWaves;
     constexpr int kOutF = SWIGLU ? NF / 2 : NF, kUnitF = kOutF < 2 ? 1 : 2;
-    constexpr int kUnitRow = kUnitF * 32 * (int)sizeof(OUT), kUnitRows = 2048 / kUnitRow < 32 ? 2048 / kUnitRow : 32;
+    constexpr int kUnitRow = kUnitF * 32 * (int)sizeof(OUT);
+    constexpr int kUnitRows = kUnit / kUnitRow < 32 ? kUnit / kUnitRow : 32;
     constexpr int kUnitStores = kUnitRows * kUnitRow / 1024;
     constexpr int kStores = MF * (32 / kUnitRows) * (kOutF / kUnitF) * kUnitStores;
     static_assert(kOutF % kUnitF == 0 && kUnitStores >= 1 && BM <= kThreads, "results");
     static_assert((STAGES - 2) * kLoads + kStores <= 63, "vmcnt has six bits");
     extern __shared__ __attribute__((aligned(1024))) int8_t s_stage[];
-    __shared__ __attribute__((aligned(16))) int8_t s_unit[kWaves][2048];
+    __shared__ __attribute__((aligned(16))) int8_t s_unit[kWaves][kUnit];
     __shared__ int32_t s_prefix[MOE_MAX_EXPERTS + 1];
     __shared__ __attribute__((aligned(16))) float s_ws[BN];
     __shared__ float s_as[BM];
     __shared__ uint32_t s_ok[BM / 32];                        // a bit for each row to be written
+    constexpr int kRing = 8;
+    static_assert(STAGES + 2 <= kRing, "tiles between the loads and the products");
+    __shared__ Tile s_tile[kRing];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
@@ -611,24 +579,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     const bool behind = (p.K & ~(kStepK - 1)) + piece >= p.K; // in a ragged last step
     u32x4 abuf, wbuf;
     uint32_t avo[kLoadsA], wvo[kLoadsW];
-    int32_t load_tile = first, load_step = 0;
+    int32_t arow[kLoadsA];                                    // read at aim(), used a step later
+    int32_t load_tile = first, load_step = 0, load_nth = 0;
     uint32_t load_to = lds0 + wave * 1024;
     int32_t ahead = 0;                                        // stages loaded and not yet begun
     int32_t older = 0;                                        // of these, before the last stores
     const auto aim = [&]() {
         const Tile t = tile_at<BM, kGroup>(p, s_prefix, load_tile);
+        if (tid == 0)
+            s_tile[load_nth % kRing] = t;
+        ++load_nth;
         abuf = p.row_token ? buffer_of(p.a, (uint32_t)((int64_t)p.a_rows * p.K))
                            : buffer_of(p.a + (int64_t)t.row0 * p.K, (uint32_t)(t.rows * p.K));
         wbuf = buffer_of(p.w + (int64_t)t.e * n_w * p.K, (uint32_t)((int64_t)n_w * p.K));
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
             const int32_t m = min(8 * (i * kWaves + wave) + line, t.rows - 1);
-            int32_t src = m;
-            if (p.row_token) {
-                src = p.row_token[t.row0 + m];
-                src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
-            }
-            avo[i] = (uint32_t)src * (uint32_t)p.K + piece;
+            arow[i] = p.row_token ? p.row_token[t.row0 + m] : m;
         }
         const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
 #pragma unroll
@@ -644,6 +611,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         if (load_tile >= last)
             return;
         const uint32_t at = (uint32_t)load_step * kStepK;
+        if (load_step == 0) {
+#pragma unroll
+            for (int i = 0; i < kLoadsA; ++i) {
+                int32_t r = arow[i];
+                if (p.row_token)
+                    r = (uint32_t)r < (uint32_t)p.a_rows ? r : 0;     // its results are not stored
+                avo[i] = (uint32_t)r * (uint32_t)p.K + piece;
+            }
+        }
         // pieces behind the end of K repeat the step's first one, and are zeroed in LDS later
         const uint32_t back = ragged && load_step == steps - 1 && behind ? piece : 0u;
 #pragma unroll
@@ -749,10 +725,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
                 i32x4{0, 0, 0, 0};
     }
     wait_workgroup();
-    for (int32_t tile = first; tile < last; tile += stride) {
+    for (int32_t tile = first, nth = 0; tile < last; tile += stride, ++nth) {
         if (steps == 1)                                       // no wait in the loop keeps the
             wait_workgroup();                                 // tiles' scales apart
-        const Tile t = tile_at<BM, kGroup>(p, s_prefix, tile);
+        Tile t;
+        t.e = __builtin_amdgcn_readfirstlane(s_tile[nth % kRing].e);
+        t.row0 = __builtin_amdgcn_readfirstlane(s_tile[nth % kRing].row0);
+        t.rows = __builtin_amdgcn_readfirstlane(s_tile[nth % kRing].rows);
+        t.n = __builtin_amdgcn_readfirstlane(s_tile[nth % kRing].n);
         // scales: a thread's row of the tile, and its channels, put into LDS at the tile's end
         const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
         const bool mine = tid < t.rows;
@@ -773,6 +753,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
                 for (int i = 0; i < 16; ++i)
                     acc[m][f][i] = 0;
         read(0, 0);
+        bool ok = false;
+        float as = 0.0f;
+        const auto scale = [&]() {
+            ok = mine && (uint32_t)src < (uint32_t)p.a_rows;
+            as = p.a_scale[ok ? src : 0];
+        };
+        if (steps < 3)
+            scale();
         for (int32_t step = 0; step < steps - 1; ++step) {
             multiply(0, 1);
             multiply(1, 2);
@@ -781,16 +769,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
             landed(next, ragged && step == steps - 2);
             wait_workgroup();                                 // and this stage is read
             --ahead;
+            if (step == 1)                                    // a wait for the row, which is there
+                scale();
             issue();
             at = next;
             multiply(1, 0);
         }
-        const bool ok = mine && (uint32_t)src < (uint32_t)p.a_rows;
-        const float as = p.a_scale[ok ? src : 0];
         multiply(0, 1);
         multiply(1, 2);
         multiply(0, 3);
         multiply(1, -1);
+        const int next = after(at);
+        if (ahead > 0)
+            landed(next, ragged && steps == 1);
         if (tid < BM)
             s_as[tid] = as;
         const uint64_t oks = __ballot(ok);
@@ -800,9 +791,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         for (int i = 0; i < (BN + kThreads - 1) / kThreads; ++i)
             if (i * kThreads + tid < BN)
                 s_ws[i * kThreads + tid] = ws[i];
-        const int next = after(at);
-        if (ahead > 0)
-            landed(next, ragged && steps == 1);
         wait_workgroup();
         older = 0;
         if (ahead > 0) {
@@ -813,7 +801,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         at = next;
 
         // Results, while the next tile's first stages are on their way: the lane's fp32 values are
-        // rounded, go through 2 KiB of LDS of the wavefront's own, and come back as rows of 128
+        // rounded, go through a little LDS of the wavefront's own, and come back as rows of 128
         // bytes (bf16) for 16-byte stores; 16-byte piece c of row r lies in slot c ^ (r % 8).
         // Stores of whole rows count the same for every wavefront, so that the loads before them
         // can be waited for without them. (Stored from the accumulators two bytes at a time, the
@@ -901,26 +889,27 @@ inline int64_t most_tiles(const MatmulArgs& p, int32_t bm)
     return p.offsets ? p.R / bm + (p.E < p.R ? p.E : p.R) : div_up(p.R, bm);
 }
 
-template <int MF, int NF, int WAVES, bool SWIGLU, typename OUT>
+template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
 bool launch_few(MatmulArgs p, hipStream_t stream)
 {
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
-    const int64_t blocks = div_up(most_tiles(p, 16 * MF) * p.n_blocks, kXcds) * kXcds;
+    const int64_t blocks = most_tiles(p, 16 * MF) * p.n_blocks;
     if (blocks * 64 * WAVES > INT32_MAX)
         return false;
-    k_matmul_few<MF, NF, WAVES, SWIGLU, OUT><<<(unsigned)blocks, 64 * WAVES, 0, stream>>>(p);
+    k_matmul_few<MF, NF, WAVES, U, SWIGLU, OUT><<<(unsigned)blocks, 64 * WAVES, 0, stream>>>(p);
     return true;
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool SWIGLU, typename OUT>
+template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, int WGS, bool SWIGLU, typename OUT>
 bool launch_tile(MatmulArgs p, hipStream_t stream)
 {
     constexpr int kThreads = 64 * WM * WN, kLds = STAGES * (BM + BN) * kStepK;
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? BN / 2 : BN);
+    p.inv_blocks = 1.0 / p.n_blocks;
     const int64_t tiles = most_tiles(p, BM) * p.n_blocks;
     if (tiles > INT32_MAX / 2)
         return false;
-    const int64_t blocks = tiles < kCus ? div_up(tiles, kXcds) * kXcds : kCus;
+    const int64_t blocks = tiles < kCus * WGS ? div_up(tiles, kXcds) * kXcds : kCus * WGS;
     const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, PIN, SWIGLU, OUT>;
     if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
                                             hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -935,10 +924,10 @@ bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
 {
     const int64_t rows = p.R / p.E;                           // of an expert, on average
     if (rows < 32)
-        return launch_few<4, 4, 4, SWIGLU, OUT>(p, stream);
+        return launch_few<2, 4, 4, 1, SWIGLU, OUT>(p, stream);
     if (rows < 160)
-        return launch_tile<128, 256, 2, 2, 3, false, SWIGLU, OUT>(p, stream);
-    return launch_tile<256, 256, 4, 2, 2, true, SWIGLU, OUT>(p, stream);
+        return launch_tile<128, 256, 2, 2, 3, false, 1, SWIGLU, OUT>(p, stream);
+    return launch_tile<256, 256, 2, 4, 2, true, 1, SWIGLU, OUT>(p, stream);
 }
 
 moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
@@ -1003,6 +992,7 @@ moe_status_t moe_expert_matmul_i8(const int8_t* a, const float* a_scale, int32_t
     p.N = N;
     p.K = K;
     p.n_blocks = 0;
+    p.inv_blocks = 0.0;
     const bool bf16 = out_dtype == MOE_BF16;
     const bool fits = act == MOE_ACT_SWIGLU ? (bf16 ? launch_matmul<true, __bf16>(p, stream)
                                                     : launch_matmul<true, float>(p, stream))
