@@ -900,6 +900,10 @@ bool launch_few(MatmulArgs p, hipStream_t stream)
     return true;
 }
 
+// WGS: persistent workgroups of a CU; kOnce: a workgroup for each tile, taken up as CUs come free
+// (the weights of 256 experts for 4 rows each: 1190 to 1236 us against 1242 to 1253).
+constexpr int kOnce = 1 << 20;
+
 template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, int WGS, bool SWIGLU, typename OUT>
 bool launch_tile(MatmulArgs p, hipStream_t stream)
 {
@@ -909,7 +913,10 @@ bool launch_tile(MatmulArgs p, hipStream_t stream)
     const int64_t tiles = most_tiles(p, BM) * p.n_blocks;
     if (tiles > INT32_MAX / 2)
         return false;
-    const int64_t blocks = tiles < kCus * WGS ? div_up(tiles, kXcds) * kXcds : kCus * WGS;
+    const int64_t most = (int64_t)kCus * WGS;
+    const int64_t blocks = tiles < most ? div_up(tiles, kXcds) * kXcds : most;
+    if (blocks * kThreads > INT32_MAX)
+        return false;
     const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, PIN, SWIGLU, OUT>;
     if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
                                             hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -919,15 +926,71 @@ bool launch_tile(MatmulArgs p, hipStream_t stream)
     return true;
 }
 
+// The tile shapes, and what a step of 128 bytes of K and a tile's beginning and end take (us, as
+// measured with every slot taken; `alone` with one workgroup a CU): 16384 channels by 4096 rows in
+// one expert, K = 2048 and 8192. Large tiles read less for each product (256 x 256: 2.2 POPS; 128 x
+// 256: 2.0; 64 x 256: 1.4), small ones waste less on experts with few rows and fill the GPU sooner.
+struct TileCost {
+    int32_t bm, bn, slots;
+    float step, alone, tile;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 256, 1.75f, 1.50f, 7.0f},
+    {128, 256, 256, 1.08f, 0.95f, 4.3f},
+    {128, 128, 512, 1.30f, 0.90f, 2.0f},
+    {64, 256, 256, 0.72f, 0.72f, 2.5f},
+    {32, 128, 512, 0.75f, 0.50f, 1.5f},
+};
+
+// The shape with the least time by these figures: rounds of tiles over the slots, where an expert's
+// last tile is half full on average. The host knows the rows of all experts, not of each.
+inline int choose_tile(const MatmulArgs& p, int64_t n_w)
+{
+    const double steps = (double)div_up(p.K, kStepK);
+    const int64_t experts = p.E < p.R ? p.E : p.R;
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < 5; ++i) {
+        const TileCost& c = kTiles[i];
+        int64_t tiles = p.offsets ? p.R / c.bm + experts / 2 : div_up(p.R, c.bm);
+        if (tiles < experts)
+            tiles = experts;
+        tiles *= div_up(n_w, c.bn);
+        const double step = tiles <= 256 ? c.alone : c.step;
+        const double time = (double)div_up(tiles, c.slots) * (steps * step + c.tile);
+        if (i == 0 || time < least) {
+            best = i;
+            least = time;
+        }
+    }
+    return best;
+}
+
+// Few tiles leave most of the GPU idle and their K axis in one workgroup: there the wavefronts of a
+// workgroup share K, and 16 or 32 channels make a workgroup (one row by 4096 channels, K = 7168:
+// 8.7 us against 28; 64 rows: 19 against 28; 128 rows, 128 tiles of 32 x 128: 33 against 28).
+constexpr int64_t kFewTiles = 128;
+
 template <bool SWIGLU, typename OUT>
 bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
 {
-    const int64_t rows = p.R / p.E;                           // of an expert, on average
-    if (rows < 32)
-        return launch_few<2, 4, 4, 1, SWIGLU, OUT>(p, stream);
-    if (rows < 160)
-        return launch_tile<128, 256, 2, 2, 3, false, 1, SWIGLU, OUT>(p, stream);
-    return launch_tile<256, 256, 2, 4, 2, true, 1, SWIGLU, OUT>(p, stream);
+    const int64_t n_w = SWIGLU ? 2 * (int64_t)p.N : p.N;
+    const int64_t experts = p.E < p.R ? p.E : p.R;
+    const int64_t rows = div_up(p.R, experts);
+    if (most_tiles(p, 32) * div_up(n_w, 128) < kFewTiles) {
+        if (rows > 16)
+            return launch_few<2, 2, 8, 2, SWIGLU, OUT>(p, stream);
+        if (SWIGLU || most_tiles(p, 16) * div_up(n_w, 16) > 512)
+            return launch_few<1, 2, 8, 4, SWIGLU, OUT>(p, stream);
+        return launch_few<1, SWIGLU ? 2 : 1, 8, 4, SWIGLU, OUT>(p, stream);
+    }
+    switch (choose_tile(p, n_w)) {
+    case 0: return launch_tile<256, 256, 2, 4, 2, true, 1, SWIGLU, OUT>(p, stream);
+    case 1: return launch_tile<128, 256, 2, 4, 3, true, 1, SWIGLU, OUT>(p, stream);
+    case 2: return launch_tile<128, 128, 2, 2, 2, true, 2, SWIGLU, OUT>(p, stream);
+    case 3: return launch_tile<64, 256, 2, 4, 3, false, 1, SWIGLU, OUT>(p, stream);
+    default: return launch_tile<32, 128, 1, 2, 3, false, kOnce, SWIGLU, OUT>(p, stream);
+    }
 }
 
 moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
