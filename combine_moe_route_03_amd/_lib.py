@@ -389,40 +389,57 @@ def moe_ep_combine_reduced(partials: torch.Tensor, part_row: torch.Tensor, out: 
 # check every tensor (device, type, shape, density) before the library sees its pointer, and run
 # on the device of their tensors whichever one is current.
 
-def _arg(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """Address of a tensor that is what the call needs; raises what is wrong with it otherwise.
+    `dtype`: one, or a tuple to choose from."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.device == device and
+            (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and
+            t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    dtypes = dtype if type(dtype) is tuple else (dtype,)
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, needs {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, the call is on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    return t
+    raise ValueError(f"{name}: not contiguous")
+
+
+def _opt(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Optional[int]:
+    return None if t is None else _arg(name, t, dtype, shape, device)
 
 
 def _matrix(name: str, t: torch.Tensor) -> torch.device:
     """The device of a call, from its main input."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name}: a 2-d tensor is needed")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: on {t.device}, needs a GPU")
     return t.device
 
 
-def _out(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _arg(name, t, dtype, shape, device)
+_MASKS = (torch.bool, torch.uint8)
+_WIDE = (torch.bfloat16, torch.float32)
 
 
 def _enqueue(fn: str, device: torch.device, stream, *args) -> None:
-    """Call a library function on `device`, on `stream` or the device's current stream."""
-    with torch.cuda.device(device):
-        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+    """Call a library function on `device`, on `stream` or the device's current stream. (The raw
+    calls below cost a tenth of torch.cuda.current_stream() and torch.cuda.device(), which took
+    more host time than the launch.)"""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == device.index:
+        status = getattr(_lib or load(), fn)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_lib or load(), fn)(*args, raw)
+    if status != MOE_OK:
+        raise MoeError(fn, status)
 
 
 def moe_balance_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
@@ -447,17 +464,17 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     dev = _matrix("logits", logits)
     T, E = logits.shape
     k = topk_idx.shape[-1]
-    _arg("logits", logits, torch.float32, (T, E), dev)
-    _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
-    if token_mask is not None:
-        _arg("token_mask", token_mask, (torch.bool, torch.uint8), (T,), dev)
     n_seqs = int(n_seqs)
     if n_seqs < 1 or T % n_seqs:
         raise ValueError(f"n_seqs: {n_seqs} sequences do not divide {T} tokens")
-    loss = _out("loss", loss, torch.float32, (1,), dev)
-    expert_counts = _out("expert_counts", expert_counts, torch.int32, (n_seqs, E), dev)
-    prob_sums = _out("prob_sums", prob_sums, torch.float32, (n_seqs, E), dev)
-    seq_tokens = _out("seq_tokens", seq_tokens, torch.int32, (n_seqs,), dev)
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    if expert_counts is None:
+        expert_counts = torch.empty((n_seqs, E), dtype=torch.int32, device=dev)
+    if prob_sums is None:
+        prob_sums = torch.empty((n_seqs, E), dtype=torch.float32, device=dev)
+    if seq_tokens is None:
+        seq_tokens = torch.empty(n_seqs, dtype=torch.int32, device=dev)
     if workspace is None:
         workspace = alloc_balance_workspace(T, E, n_seqs, dev)
         if isinstance(stream, torch.cuda.Stream):
@@ -466,9 +483,15 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
             workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=dev))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: needs contiguous memory on {dev}")
-    _enqueue("moe_balance_loss", dev, stream, _ptr(logits), _ptr(topk_idx), _ptr(token_mask), T, E,
-             k, n_seqs, float(alpha), _ptr(loss), _ptr(expert_counts), _ptr(prob_sums),
-             _ptr(seq_tokens), _ptr(workspace), workspace.numel() * workspace.element_size())
+    _enqueue("moe_balance_loss", dev, stream,
+             _arg("logits", logits, torch.float32, (T, E), dev),
+             _arg("topk_idx", topk_idx, torch.int32, (T, k), dev),
+             _opt("token_mask", token_mask, _MASKS, (T,), dev), T, E, k, n_seqs, float(alpha),
+             _arg("loss", loss, torch.float32, (1,), dev),
+             _arg("expert_counts", expert_counts, torch.int32, (n_seqs, E), dev),
+             _arg("prob_sums", prob_sums, torch.float32, (n_seqs, E), dev),
+             _arg("seq_tokens", seq_tokens, torch.int32, (n_seqs,), dev),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return loss, expert_counts, prob_sums, seq_tokens
 
 
@@ -485,20 +508,18 @@ def moe_route_grad(logits: torch.Tensor, topk_idx: torch.Tensor,
     T, E = logits.shape
     k = topk_idx.shape[-1]
     n_seqs = int(n_seqs)
-    _arg("logits", logits, torch.float32, (T, E), dev)
-    _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
-    for name, t, dtypes, shape in (
-            ("topk_w", topk_w, torch.float32, (T, k)), ("dtopk_w", dtopk_w, torch.float32, (T, k)),
-            ("token_mask", token_mask, (torch.bool, torch.uint8), (T,)),
-            ("expert_counts", expert_counts, torch.int32, (n_seqs, E)),
-            ("seq_tokens", seq_tokens, torch.int32, (n_seqs,)),
-            ("dloss", dloss, torch.float32, (1,))):
-        if t is not None:
-            _arg(name, t, dtypes, shape, dev)
-    dlogits = _out("dlogits", dlogits, torch.float32, (T, E), dev)
-    _enqueue("moe_route_grad", dev, stream, _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
-             _ptr(dtopk_w), _ptr(token_mask), _ptr(expert_counts), _ptr(seq_tokens), _ptr(dloss),
-             T, E, k, n_seqs, float(alpha), _ptr(dlogits))
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _enqueue("moe_route_grad", dev, stream,
+             _arg("logits", logits, torch.float32, (T, E), dev),
+             _arg("topk_idx", topk_idx, torch.int32, (T, k), dev),
+             _opt("topk_w", topk_w, torch.float32, (T, k), dev),
+             _opt("dtopk_w", dtopk_w, torch.float32, (T, k), dev),
+             _opt("token_mask", token_mask, _MASKS, (T,), dev),
+             _opt("expert_counts", expert_counts, torch.int32, (n_seqs, E), dev),
+             _opt("seq_tokens", seq_tokens, torch.int32, (n_seqs,), dev),
+             _opt("dloss", dloss, torch.float32, (1,), dev), T, E, k, n_seqs, float(alpha),
+             _arg("dlogits", dlogits, torch.float32, (T, E), dev))
     return dlogits
 
 
@@ -509,13 +530,13 @@ def moe_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     the device): only the first n_rows rows are quantised."""
     dev = _matrix("x", x)
     R, H = x.shape
-    _arg("x", x, (torch.bfloat16, torch.float32), (R, H), dev)
-    q = _out("q", q, torch.int8, (R, H), dev)
-    scale = _out("scale", scale, torch.float32, (R,), dev)
-    if n_rows is not None:
-        _arg("n_rows", n_rows, torch.int32, (1,), dev)
-    _enqueue("moe_quant_rows", dev, stream, _ptr(x), _dtype_code(x), R, H, _ptr(n_rows), _ptr(q),
-             _ptr(scale))
+    if q is None:
+        q = torch.empty((R, H), dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(R, dtype=torch.float32, device=dev)
+    _enqueue("moe_quant_rows", dev, stream, _arg("x", x, _WIDE, (R, H), dev), _dtype_code(x), R, H,
+             _opt("n_rows", n_rows, torch.int32, (1,), dev), _arg("q", q, torch.int8, (R, H), dev),
+             _arg("scale", scale, torch.float32, (R,), dev))
     return q, scale
 
 
@@ -539,18 +560,13 @@ def moe_expert_matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor
         raise ValueError(f"w: {n_w} channels do not split into gate and up")
     N = n_w // 2 if act == "swiglu" else n_w
     R = A if row_token is None else row_token.numel()
-    _arg("a", a, torch.int8, (A, K), dev)
-    _arg("a_scale", a_scale, torch.float32, (A,), dev)
-    _arg("w", w, torch.int8, (E, n_w, K), dev)
-    _arg("w_scale", w_scale, torch.float32, (E, n_w), dev)
-    if expert_offsets is not None:
-        _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev)
-    if row_token is not None:
-        _arg("row_token", row_token, torch.int32, (R,), dev)
     if out is None:
         out = torch.empty((R, N), dtype=out_dtype, device=dev)
-    _arg("out", out, (torch.bfloat16, torch.float32), (R, N), dev)
-    _enqueue("moe_expert_matmul_i8", dev, stream, _ptr(a), _ptr(a_scale), A, _ptr(row_token),
-             _ptr(w), _ptr(w_scale), _ptr(expert_offsets), R, E, N, K, ACT_CODES[act], _ptr(out),
-             _dtype_code(out))
+    _enqueue("moe_expert_matmul_i8", dev, stream, _arg("a", a, torch.int8, (A, K), dev),
+             _arg("a_scale", a_scale, torch.float32, (A,), dev), A,
+             _opt("row_token", row_token, torch.int32, (R,), dev),
+             _arg("w", w, torch.int8, (E, n_w, K), dev),
+             _arg("w_scale", w_scale, torch.float32, (E, n_w), dev),
+             _opt("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev), R, E, N, K,
+             ACT_CODES[act], _arg("out", out, _WIDE, (R, N), dev), _dtype_code(out))
     return out
