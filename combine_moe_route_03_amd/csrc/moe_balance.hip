@@ -14,12 +14,14 @@ namespace {
 
 using namespace moe_dev;
 
-constexpr int kLossThreads = 512;
+constexpr int kLossThreads = 1024;
 constexpr int kLossWaves = kLossThreads / 64;
 constexpr int kGradThreads = 256;
-constexpr int kMaxLossBlocks = 512;      // workgroups of the forward pass, about two a CU
-constexpr int kFinishExperts = 16;       // experts of a finishing workgroup
-constexpr int kFinishThreads = 256;      //   by 16 slices of the partial sums
+constexpr int kMaxLossBlocks = 512;      // workgroups of the forward pass, two a CU
+constexpr int kLossTokens = 32;          //   of no fewer tokens than two a wavefront
+constexpr int kDirectTokens = 192;       // one workgroup and one launch up to so many tokens
+constexpr int kFinishExperts = 64;       // experts of a finishing workgroup
+constexpr int kFinishThreads = 512;      //   by 8 slices of the partial sums
 constexpr int kFinishSlices = kFinishThreads / kFinishExperts;
 
 // A row of E fp32 values over the G lanes of a group: lane g holds elements (v * G + g) * VEC + c.
@@ -62,24 +64,20 @@ struct Row {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     x[c] = v[i * VEC + c];
-                *reinterpret_cast<f32x4*>(p + e) = x;
+                __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(p + e));
             } else {
-                p[e] = v[i];
+                __builtin_nontemporal_store(v[i], p + e);
             }
         }
     }
 };
 
-// exp(x) for x <= 0 as 2^(x log2 e), the product in two parts: with one part its rounding alone
-// would give a relative error of |x| 2^-24. v_exp_f32 is good to one ulp. Results below 2^-126 are
-// zero (as v_exp_f32 has them); next to the row's largest term, which is 1, they are nothing.
+// exp(x) for x <= 0 as 2^(x log2 e), log2 e in two parts: off by |x| 2^-24 for the product's
+// rounding, and by one ulp of v_exp_f32. Results below 2^-126 are zero; next to the row's largest
+// term, which is 1, they are nothing.
 __device__ __forceinline__ float exp_neg(float x)
 {
-    constexpr float hi = 1.44269502f, lo = 1.92596299e-8f;
-    const float t = x * hi;
-    const float rest = __builtin_fmaf(x, hi, -t) + x * lo;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return x < -87.0f ? 0.0f : __builtin_fmaf(e, rest * 0.693147182f, e);
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, 1.44269502f, x * 1.92596299e-8f));
 }
 
 // Turns logits into probabilities in place. A row of -infinity only gets zeros; a NaN or +infinity
@@ -101,7 +99,7 @@ __device__ __forceinline__ void softmax_row(Row<G, NV, VEC>& r)
         s += r.v[i];
     }
     s = group_sum<G>(s);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+    const float inv = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);    // one ulp
 #pragma unroll
     for (int i = 0; i < NV * VEC; ++i)
         r.v[i] *= inv;
@@ -173,16 +171,27 @@ __global__ __launch_bounds__(kLossThreads) void k_balance_partial(LossArgs a)
     for (int i = 0; i < NV * VEC; ++i)
         sum.v[i] = 0.0f;
     int seen = 0;
-    for (int t = grp; t < n; t += kGroups) {
-        if (a.mask && !a.mask[first + t])
-            continue;
-        Row<G, NV, VEC> r;
-        r.load(a.logits + (first + t) * a.E, g, a.E);
-        softmax_row(r);
+    constexpr int U = NV * VEC <= 4 ? 4 : NV * VEC <= 8 ? 2 : 1;      // rows in flight
+    for (int t0 = grp; t0 < n; t0 += U * kGroups) {
+        Row<G, NV, VEC> r[U];
+        bool use[U];
 #pragma unroll
-        for (int i = 0; i < NV * VEC; ++i)
-            sum.v[i] += r.v[i];
-        ++seen;
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u * kGroups;
+            use[u] = t < n && (!a.mask || a.mask[first + t]);
+            if (use[u])
+                r[u].load(a.logits + (first + t) * a.E, g, a.E);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!use[u])
+                continue;
+            softmax_row(r[u]);
+#pragma unroll
+            for (int i = 0; i < NV * VEC; ++i)
+                sum.v[i] += r[u].v[i];
+            ++seen;
+        }
     }
     if (g == 0 && seen)
         atomicAdd(&s_tokens, seen);
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(kLossThreads) void k_balance_partial(LossArgs a)
     }
 }
 
-// Sums the workgroups' parts of 16 experts of one sequence (16 slices side by side, joined in
+// Sums the workgroups' parts of 64 experts of one sequence (8 slices side by side, joined in
 // order, fp64) and its share of the loss; the last workgroup to finish adds the shares up in their
 // order. The shares cross XCDs, whose L2s are not coherent, so they are stored and loaded at
 // device scope.
@@ -257,10 +266,26 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(LossArgs a, i
     double p = 0.0;
     int32_t n = 0;
     if (e < a.E) {
-        for (int b = slice; b < a.nb; b += kFinishSlices) {
-            const int64_t at = ((int64_t)s * a.nb + b) * a.E + e;
-            p += a.part_sum[at];
-            n += a.part_count[at];
+        const float* sum = a.part_sum + (int64_t)s * a.nb * a.E + e;
+        const int32_t* count = a.part_count + (int64_t)s * a.nb * a.E + e;
+        int b = slice;
+        for (; b + 3 * kFinishSlices < a.nb; b += 4 * kFinishSlices) {
+            float x[4];
+            int32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = sum[(int64_t)(b + i * kFinishSlices) * a.E];
+                c[i] = count[(int64_t)(b + i * kFinishSlices) * a.E];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p += x[i];
+                n += c[i];
+            }
+        }
+        for (; b < a.nb; b += kFinishSlices) {
+            p += sum[(int64_t)b * a.E];
+            n += count[(int64_t)b * a.E];
         }
     }
     s_sum[tid] = p;
@@ -274,6 +299,7 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(LossArgs a, i
     tokens = s_tokens;
     double dot = 0.0;
     if (tid < kFinishExperts && e < a.E) {
+#pragma unroll 1
         for (int i = 1; i < kFinishSlices; ++i) {
             p += s_sum[i * kFinishExperts + tid];
             n += s_count[i * kFinishExperts + tid];
@@ -288,6 +314,7 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(LossArgs a, i
     __syncthreads();
     if (tid == 0) {
         double all = 0.0;
+#pragma unroll 8
         for (int i = 0; i < kFinishExperts; ++i)
             all += s_sum[i];
         if (c == 0)
@@ -342,16 +369,23 @@ struct GradArgs {
     float* out;
 };
 
-// G lanes take a token at a time: softmax of its logits, the two reductions, one store. The counts
-// enter as c - m with the integer m nearest to the mean count k n / E: the probabilities add up to
-// one, so m drops out, and the difference p (c - sum c p) loses nothing to cancellation (the plain
-// difference loses log2(c / |c - mean|) bits). A group keeps its sequence's centred counts in
-// registers while its tokens stay in the sequence.
+// G lanes take a token at a time: softmax of its logits, the two reductions, one store (past the
+// caches: 65536 tokens of 256 experts 29 us against 38 with plain stores; two or four tokens in
+// flight for a group cost more in occupancy than they hide, 33 and 48 us). The counts enter as
+// c - m with the integer m nearest to the mean count k n / E: the probabilities add up to one, so m
+// drops out, and the difference p (c - sum c p) loses nothing to cancellation (the plain difference
+// loses log2(c / |c - mean|) bits). A group keeps its sequence's centred counts in registers while
+// its tokens stay in the sequence.
+//   The weights' term goes through LDS of the group's own: the row is put there, the lanes of the
+// slots add theirs to it, and it is taken back (comparing every slot with every lane's experts in
+// registers took 17 us more at 65536 tokens, k = 8).
 template <int G, int NV, int VEC>
 __global__ __launch_bounds__(kGradThreads) void k_route_grad(GradArgs a)
 {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int g = lane & (G - 1);
+    const int tid = threadIdx.x;
+    const int g = tid & (G - 1);
+    __shared__ __attribute__((aligned(16))) float s_row[kGradThreads * NV * VEC];
+    float* row = s_row + tid / G * (G * NV * VEC);
     const int64_t groups = (int64_t)gridDim.x * (kGradThreads / G);
     const float dloss = a.dloss ? a.dloss[0] : 1.0f;
     int cur = -1;
@@ -359,6 +393,10 @@ __global__ __launch_bounds__(kGradThreads) void k_route_grad(GradArgs a)
     Row<G, NV, VEC> c;
     for (int64_t t = (int64_t)blockIdx.x * (kGradThreads / G) + tid / G; t < a.T; t += groups) {
         Row<G, NV, VEC> r;
+        const bool slot = a.dw && g < a.k;
+        int32_t id = slot ? a.idx[t * a.k + g] : -1;
+        float w = slot ? a.w[t * a.k + g] : 0.0f;
+        float dw = slot ? a.dw[t * a.k + g] : 0.0f;
         if (a.counts && (!a.mask || a.mask[t])) {
             r.load(a.logits + t * a.E, g, a.E);
             const int s = (int)((uint32_t)t / (uint32_t)a.L);
@@ -388,28 +426,34 @@ __global__ __launch_bounds__(kGradThreads) void k_route_grad(GradArgs a)
                 r.v[i] = 0.0f;
         }
         if (a.dw) {
-            const int32_t* idx = a.idx + t * a.k;
-            const float* w = a.w + t * a.k;
-            const float* dw = a.dw + t * a.k;
-            float part = 0.0f;
-            for (int j = g; j < a.k; j += G)
-                part = __builtin_fmaf(w[j], dw[j], part);
+            float part = w * dw;
+            for (int j = g + G; j < a.k; j += G)
+                part = __builtin_fmaf(a.w[t * a.k + j], a.dw[t * a.k + j], part);
             const float all = group_sum<G>(part);
-            for (int j = 0; j < a.k; ++j) {
-                const int id = idx[j];
-                const float add = w[j] * (dw[j] - all);
 #pragma unroll
-                for (int i = 0; i < NV * VEC; ++i)
-                    if (Row<G, NV, VEC>::expert(g, i) == id)
-                        r.v[i] += add;
+            for (int i = 0; i < NV * VEC; ++i)
+                row[Row<G, NV, VEC>::expert(g, i)] = r.v[i];
+            asm volatile("" ::: "memory");                    // LDS serves a wavefront in order
+            if ((uint32_t)id < (uint32_t)a.E)
+                __hip_atomic_fetch_add(row + id, w * (dw - all), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+            for (int j = g + G; j < a.k; j += G) {            // more slots than lanes
+                id = a.idx[t * a.k + j];
+                if ((uint32_t)id < (uint32_t)a.E)
+                    __hip_atomic_fetch_add(row + id, a.w[t * a.k + j] * (a.dw[t * a.k + j] - all),
+                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
             }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < NV * VEC; ++i)
+                r.v[i] = row[Row<G, NV, VEC>::expert(g, i)];
         }
         r.store(a.out + t * a.E, g, a.E);
     }
 }
 
-// Workgroups of a sequence, and their tokens: as many as fill the GPU twice over, but chunks of no
-// fewer than 16 tokens.
+// Workgroups of a sequence, and their tokens: as many as fill the GPU, but chunks of no fewer than
+// two tokens a wavefront; a small batch is one chunk.
 struct LossPlan {
     int32_t nb, chunk;
     size_t sum, count, tokens, loss, ticket, bytes;
@@ -420,9 +464,9 @@ LossPlan loss_plan(int32_t T, int32_t E, int32_t S)
     LossPlan p;
     const int64_t L = T / S;
     int64_t nb = kMaxLossBlocks / (S < kMaxLossBlocks ? S : kMaxLossBlocks);
-    if (nb > div_up(L, 16))
-        nb = div_up(L, 16);
-    if (nb < 1)
+    if (nb > div_up(L, kLossTokens))
+        nb = div_up(L, kLossTokens);
+    if (nb < 1 || (S == 1 && L <= kDirectTokens))
         nb = 1;
     p.chunk = (int32_t)div_up(L > 0 ? L : 1, nb);
     p.nb = (int32_t)(L > 0 ? div_up(L, p.chunk) : 1);
@@ -477,7 +521,7 @@ template <int G, int NV, int VEC>
 void launch_grad(Row<G, NV, VEC>, const GradArgs& a, hipStream_t stream)
 {
     const int64_t blocks = div_up(a.T, kGradThreads / G);
-    const int64_t most = 256 * 8;
+    const int64_t most = 4096;
     k_route_grad<G, NV, VEC><<<(unsigned)(blocks < most ? blocks : most), kGradThreads, 0,
                                stream>>>(a);
 }

@@ -23,8 +23,8 @@ __device__ __forceinline__ float dpp_f32(float v)
 
 // Reduction over groups of G lanes (a power of two), the result in every lane of the group:
 // quad_perm [1,0,3,2] and [2,3,0,1], then row_half_mirror and row_mirror pair lanes whose partial
-// results are already uniform; beyond a 16-lane row, lane exchanges through LDS hardware. The
-// order is fixed.
+// results are already uniform; beyond a 16-lane row v_permlane16_swap and v_permlane32_swap hand
+// every lane both halves' results. The order is fixed.
 template <int G, typename Op>
 __device__ __forceinline__ float group_reduce(float v, Op op)
 {
@@ -36,10 +36,16 @@ __device__ __forceinline__ float group_reduce(float v, Op op)
         v = op(v, dpp_f32<0x141>(v));
     if (G >= 16)
         v = op(v, dpp_f32<0x140>(v));
-    if (G >= 32)
-        v = op(v, __shfl_xor(v, 16));
-    if (G >= 64)
-        v = op(v, __shfl_xor(v, 32));
+    if (G >= 32) {
+        const uint32_t b = __float_as_uint(v);
+        const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    if (G >= 64) {
+        const uint32_t b = __float_as_uint(v);
+        const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
     return v;
 }
 

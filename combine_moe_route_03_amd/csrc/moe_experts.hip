@@ -10,72 +10,152 @@ using namespace moe_dev;
 // ------------------------------------------------------------------------------ 8-bit rows --
 // a = max |x|, q = rint(127 x / a), scale = a / 127. Each row is read once, held in registers
 // between its maximum and its codes, and bound by HBM: 2 (bf16) or 4 (fp32) bytes in and one out
-// for an element. G lanes take a row, with up to NV vectors of 8 elements a lane; longer rows are
-// read a second time, from the cache.
+// for an element. G lanes take a row, with up to NV vectors of 8 elements a lane in flight at once.
+// Rows beyond 512 lanes of 8 vectors are read a second time, from the cache.
 constexpr int kQuantVec = 8;
 constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
 constexpr int kCus = 256;
 
-template <typename X>
-__device__ __forceinline__ void load8(const X* __restrict__ p, float v[8]);
+// Eight elements as they are in memory.
+struct Bf16x8 {
+    typedef uint16_t elem;
+    static constexpr bool kWide = true;      // 127 x is formed, and a divides it
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u32x4 x;
 
-template <>
-__device__ __forceinline__ void load8(const uint16_t* __restrict__ p, float v[8])
-{
-    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+    __device__ __forceinline__ void load(const elem* __restrict__ p)
+    {
+        x = *reinterpret_cast<const u32x4*>(p);
+    }
+
+    // The largest magnitude: magnitudes compare as their bits do, NaN and infinity come out on top.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(x[i] << 16);
-        v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = x[i] & 0x7FFF7FFFu;
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, b));
+        }
+        return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
     }
-}
 
-template <>
-__device__ __forceinline__ void load8(const float* __restrict__ p, float v[8])
-{
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(p);
-    const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 4);
+    __device__ __forceinline__ float value(int i) const
+    {
+        return __uint_as_float(i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16);
+    }
+};
+
+struct F32x8 {
+    typedef float elem;
+    static constexpr bool kWide = false;     // 127 / a is formed, and multiplies x
+    u32x4 x[2];
+
+    __device__ __forceinline__ void load(const elem* __restrict__ p)
+    {
+        x[0] = reinterpret_cast<const u32x4*>(p)[0];
+        x[1] = reinterpret_cast<const u32x4*>(p)[1];
+    }
+
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = lo[i];
-        v[4 + i] = hi[i];
+        for (int i = 0; i < 8; ++i)
+            m = max(m, x[i / 4][i % 4] & 0x7FFFFFFFu);
+        return m;
     }
-}
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+    __device__ __forceinline__ float value(int i) const
+    {
+        return __uint_as_float(x[i / 4][i % 4]);
+    }
+};
 
-// The code of x in a row of largest magnitude a, from inv = fl(127 / a) (x and a scaled by a power
-// of two where a is tiny). fl(x inv) lies within 127 * 2^-23 of 127 x / a, so its rounding is right
-// unless it lies that near to a half; there 127 x - r a decides, which fp64 holds exactly: 127 x
-// has 31 bits, r a too, and x >= a / 254 there, so both are multiples of ulp(a) 2^-8 below 2 a.
-__device__ __forceinline__ int32_t code_of(float x, float a, float inv)
+// A row's largest magnitude, and what its codes are made with: x and a are taken times `up`, a power
+// of two (1 but for extreme a), which keeps 127 x and the reciprocals in range.
+struct Scaling {
+    float a, inv, up;
+};
+
+// The lowest byte of fl(q + 1.5 * 2^23), for four q and four more: there the whole number nearest
+// to q stands in the lowest bits, halves to even.
+__device__ __forceinline__ u32x2 low_bytes(const float t[8])
 {
-    const float q = x * inv;
-    float r = rintf(q);
-    if (__builtin_fabsf(__builtin_fabsf(q - r) - 0.5f) < 6.0e-5f) {
-        r = floorf(q);                                        // r or r + 1
-        const double d = 2.0 * (127.0 * (double)x - (double)r * (double)a) - (double)a;
-        if (d > 0.0 || (d == 0.0 && ((int32_t)r & 1)))
-            r += 1.0f;
+    u32x2 c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        c[i] = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 1]), __float_as_uint(t[4 * i]),
+                                     0x0C0C0400u) |
+               __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 3]), __float_as_uint(t[4 * i + 2]),
+                                     0x04000C0Cu);
+    return c;
+}
+constexpr float kWhole = 12582912.0f;
+
+// bf16: with 15 and 8 bits, 127 x / a is a half exactly, or at least 2^-16 of itself away from one.
+// One step of division (remainder, exact, times the reciprocal) brings the quotient to within an ulp
+// and an exact half to itself, so every code is right. (Exact halves are common: x = a / 2 is one.
+// Sent to a slower exact path they made it 45 us for 32768 rows of 2048.)
+__device__ __forceinline__ u32x2 codes8(const Bf16x8& v, const Scaling& s, bool* border)
+{
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = v.value(i) * (127.0f * s.up);
+        const float q = x * s.inv;
+        t[i] = __builtin_fmaf(__builtin_fmaf(-q, s.a, x), s.inv, q) + kWhole;
     }
-    return (int32_t)r;
+    *border = false;
+    return low_bytes(t);
 }
 
-__device__ __forceinline__ u32x2 codes8(const float v[8], float a, float inv, float up)
+// fp32: x inv, inv = fl(127 / a), is off by at most 127 * 2^-24 < 7.6e-6 from 127 x / a. Where one
+// of the elements lies that near to a half, or the row is scaled, all 8 are left to exact_codes8().
+__device__ __forceinline__ u32x2 codes8(const F32x8& v, const Scaling& s, bool* border)
+{
+    float t[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = v.value(i);
+        t[i] = __builtin_fmaf(x, s.inv, kWhole);
+        far = fmaxf(far, __builtin_fabsf(__builtin_fmaf(x, s.inv, kWhole - t[i])));
+    }
+    *border = far > 0.49999f || s.up != 1.0f;
+    return low_bytes(t);
+}
+
+// Next to a half the whole number r below the quotient or the one above it: 127 x - r a decides,
+// which fp64 holds exactly: 127 x has 31 bits, r a too, and there x >= a / 254, so both are
+// multiples of ulp(a) 2^-8 below 2 a.
+__device__ __forceinline__ u32x2 exact_codes8(const F32x8& v, const Scaling& s)
 {
     u32x2 c = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        c[i >> 2] |= ((uint32_t)code_of(v[i] * up, a, inv) & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) {
+        const float x = v.value(i) * s.up, q = x * s.inv;
+        float r = rintf(q);
+        if (__builtin_fabsf(q - r) > 0.4999f) {
+            r = floorf(q);
+            const double d = 2.0 * (127.0 * (double)x - (double)r * (double)s.a) - (double)s.a;
+            if (d > 0.0 || (d == 0.0 && ((int32_t)r & 1)))
+                r += 1.0f;
+        }
+        c[i / 4] |= ((uint32_t)(int32_t)r & 0xFFu) << (8 * (i % 4));
+    }
     return c;
 }
 
-template <typename X, int G, int NV>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_quant_rows(const X* __restrict__ x,
-                                                                  int32_t R, int32_t H,
-                                                                  const int32_t* __restrict__ n_rows,
-                                                                  int8_t* __restrict__ q,
-                                                                  float* __restrict__ scale)
+__device__ __forceinline__ u32x2 exact_codes8(const Bf16x8& v, const Scaling& s)
+{
+    bool border;
+    return codes8(v, s, &border);
+}
+
+template <typename V, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_quant_rows(
+    const typename V::elem* __restrict__ x, int32_t R, int32_t H,
+    const int32_t* __restrict__ n_rows, int8_t* __restrict__ q, float* __restrict__ scale)
 {
     constexpr int kThreads = G < 256 ? 256 : G;
     constexpr int kRows = kThreads / G;                       // rows of a workgroup at a time
@@ -88,34 +168,25 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_quant_rows(const X* __res
     for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
         const int64_t row = r0 + tid / G;
         const bool live = row < rows;
-        const X* p = x + row * H;
-        float v[NV][kQuantVec];
+        const typename V::elem* p = x + row * H;
+        V v[NV];
         uint32_t m = 0u;
         if (live) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (g + i * G < nvec) {
-                    load8(p + (int64_t)(g + i * G) * kQuantVec, v[i]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kQuantVec; ++c)
-                        v[i][c] = 0.0f;
-                }
-            }
+            for (int i = 0; i < NV; ++i)
+                if (g + i * G < nvec)
+                    v[i].load(p + (int64_t)(g + i * G) * kQuantVec);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int c = 0; c < kQuantVec; ++c)
-                    m = max(m, abs_bits(v[i][c]));
+                if (g + i * G < nvec)
+                    m = max(m, v[i].top());
             for (int i = g + NV * G; i < nvec; i += G) {
-                float t[kQuantVec];
-                load8(p + (int64_t)i * kQuantVec, t);
-#pragma unroll
-                for (int c = 0; c < kQuantVec; ++c)
-                    m = max(m, abs_bits(t[c]));
+                V t;
+                t.load(p + (int64_t)i * kQuantVec);
+                m = max(m, t.top());
             }
         }
-        // magnitudes compare as their bits do; NaN and infinity come out on top
+        // bits of magnitudes up to that of NaN order as floats do not: reduced as integers
 #pragma unroll
         for (int d = 1; d < (G < 64 ? G : 64); d <<= 1)
             m = max(m, (uint32_t)__shfl_xor((int)m, d));
@@ -131,57 +202,81 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_quant_rows(const X* __res
         }
         if (!live)
             continue;
-        float a = __uint_as_float(m), up = 1.0f, s = 1.0f, inv = 0.0f;
+        Scaling sc = {__uint_as_float(m), 0.0f, 1.0f};
+        float s = 1.0f;
         if (m >= 0x7F800000u) {
             s = __uint_as_float(0x7FC00000u);
         } else if (m) {
-            s = a / 127.0f;
-            if (a < 5.42101086e-20f)                          // 2^-64: keep 127 / a finite
-                up = 18446744073709551616.0f;                 // 2^64, exact
-            a *= up;
-            inv = 127.0f / a;
+            s = sc.a / 127.0f;
+            if (sc.a < 5.42101086e-20f)                       // 2^-64
+                sc.up = 18446744073709551616.0f;              // 2^64
+            else if (V::kWide && sc.a > 1.26765060e+30f)      // 2^100
+                sc.up = 5.42101086e-20f;
+            sc.a *= sc.up;
+            sc.inv = (V::kWide ? 1.0f : 127.0f) / sc.a;
         }
         if (g == 0)
             scale[row] = s;
-        const bool zero = inv == 0.0f;
+        const bool zero = sc.inv == 0.0f;
         int8_t* out = q + row * H;
+        uint32_t again = 0u;                                  // a bit for each vector
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (g + i * G < nvec)
+            if (g + i * G < nvec) {
+                bool border;
+                const u32x2 c = codes8(v[i], sc, &border);
+                again |= (uint32_t)(border && !zero) << i;
                 *reinterpret_cast<u32x2*>(out + (int64_t)(g + i * G) * kQuantVec) =
-                    zero ? u32x2{0u, 0u} : codes8(v[i], a, inv, up);
+                    zero ? u32x2{0u, 0u} : c;
+            }
+        // the few vectors with an element next to a half, from memory, so that this stays small
+        while (again) {
+            const int at = g + (__ffs((int)again) - 1) * G;
+            again &= again - 1u;
+            V t;
+            t.load(p + (int64_t)at * kQuantVec);
+            *reinterpret_cast<u32x2*>(out + (int64_t)at * kQuantVec) = exact_codes8(t, sc);
+        }
         for (int i = g + NV * G; i < nvec; i += G) {
-            float t[kQuantVec];
-            load8(p + (int64_t)i * kQuantVec, t);
+            V t;
+            t.load(p + (int64_t)i * kQuantVec);
             *reinterpret_cast<u32x2*>(out + (int64_t)i * kQuantVec) =
-                zero ? u32x2{0u, 0u} : codes8(t, a, inv, up);
+                zero ? u32x2{0u, 0u} : exact_codes8(t, sc);
         }
     }
 }
 
-template <typename X, int G, int NV>
+template <typename V, int G, int NV>
 void launch_quant_g(const void* x, int32_t R, int32_t H, const int32_t* n_rows, int8_t* q,
                     float* scale, hipStream_t stream)
 {
     constexpr int kThreads = G < 256 ? 256 : G;
     const int64_t blocks = div_up(R, kThreads / G);
     const int64_t most = 1 << 20;
-    k_quant_rows<X, G, NV><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, stream>>>(
-        static_cast<const X*>(x), R, H, n_rows, q, scale);
+    k_quant_rows<V, G, NV><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, stream>>>(
+        static_cast<const typename V::elem*>(x), R, H, n_rows, q, scale);
 }
 
-template <typename X>
+// Lanes of a row: few enough that each has two to four vectors in flight, so many that a row's
+// registers leave room for other rows. 32768 rows in bf16: 1408 elements 30 us with 64 lanes, 33
+// with 128, 37 with 256; 2048: 40, 39, 44; 4096: 81, 73, 73 (5.5 TB/s), 91 with 512; 4096 rows of
+// 7168: 20, 20, 18, 18.
+template <typename V>
 void launch_quant(const void* x, int32_t R, int32_t H, const int32_t* n_rows, int8_t* q,
                   float* scale, hipStream_t stream)
 {
-    if (H <= 16 * 4 * kQuantVec)
-        launch_quant_g<X, 16, 4>(x, R, H, n_rows, q, scale, stream);
-    else if (H <= 64 * 4 * kQuantVec)
-        launch_quant_g<X, 64, 4>(x, R, H, n_rows, q, scale, stream);
-    else if (H <= 256 * 4 * kQuantVec)
-        launch_quant_g<X, 256, 4>(x, R, H, n_rows, q, scale, stream);
+    if (H <= 512)
+        launch_quant_g<V, 16, 4>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 1536)
+        launch_quant_g<V, 64, 4>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 2048)
+        launch_quant_g<V, 128, 2>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 4096)
+        launch_quant_g<V, 128, 4>(x, R, H, n_rows, q, scale, stream);
+    else if (H <= 8192)
+        launch_quant_g<V, 512, 2>(x, R, H, n_rows, q, scale, stream);
     else
-        launch_quant_g<X, 1024, 4>(x, R, H, n_rows, q, scale, stream);
+        launch_quant_g<V, 512, 8>(x, R, H, n_rows, q, scale, stream);
 }
 
 // ------------------------------------------------------------------------ experts' product --
@@ -1013,9 +1108,9 @@ moe_status_t moe_quant_rows(const void* x, moe_dtype_t x_dtype, int32_t R, int32
     if (R == 0)
         return MOE_OK;
     if (x_dtype == MOE_BF16)
-        launch_quant<uint16_t>(x, R, H, n_rows, q, scale, stream);
+        launch_quant<Bf16x8>(x, R, H, n_rows, q, scale, stream);
     else
-        launch_quant<float>(x, R, H, n_rows, q, scale, stream);
+        launch_quant<F32x8>(x, R, H, n_rows, q, scale, stream);
     return launched();
 }
 

@@ -60,8 +60,8 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* topk_idx,
  * with g = dloss[0] (fp32 on the device; NULL: 1). The counts are constants of the loss. Counts
  * and tokens may have been summed over devices first: the loss is then that of the joint batch.
  *   topk_w, dtopk_w [T, k] fp32: the weights of moe_route_topk and the gradient that reached them.
- *   topk_idx is read only for the weights; slots outside [0, E) are skipped, equal ids add up in
- *   slot order. logits and token_mask are read only for the loss.
+ *   topk_idx is read only for the weights; slots outside [0, E) are skipped, equal ids add up.
+ *   logits and token_mask are read only for the loss.
  *   dlogits [T, E] fp32 out, every element written.
  * Sizes as for moe_balance_loss; expert_counts and seq_tokens are given together, topk_w and
  * dtopk_w too, and one pair at least (else MOE_ERR_INVALID). T = 0 enqueues nothing.
