@@ -7,6 +7,7 @@ ImportError; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -442,6 +443,7 @@ def _enqueue(fn: str, device: torch.device, stream, *args) -> None:
         raise MoeError(fn, status)
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_balance_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
     return int(load().moe_balance_workspace_bytes(T, E, n_seqs))
 
