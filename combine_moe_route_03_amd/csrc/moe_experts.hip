@@ -1,5 +1,7 @@
 // moe_experts.hip -- 8-bit rows with a scale for each token, and the experts' product in 8-bit
 // integers (declared in include/moe_layer.h).
+#include <atomic>
+
 #include "moe_device.h"
 #include "moe_layer.h"
 
@@ -290,6 +292,7 @@ struct MatmulArgs {
     void* out;
     int32_t a_rows, R, E, N, K;
     int32_t n_blocks;          // workgroups side by side over the channels
+    int32_t max_tiles;         // row tiles, at most
     double inv_blocks;         // 1 / n_blocks
 };
 
@@ -541,11 +544,11 @@ __device__ __forceinline__ void store_buffer(u32x4 v, __amdgpu_buffer_rsrc_t buf
 }
 
 // Exclusive prefix of the experts' row tiles into prefix[0 .. E] (every thread calls), and their
-// total.
+// total; 0 if that is more than rising offsets can give.
 template <int THREADS, int BM>
 __device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* prefix)
 {
-    __shared__ int32_t s_wave[THREADS / 64];
+    __shared__ int64_t s_wave[THREADS / 64];
     const int tid = threadIdx.x;
     const int per = (p.E + THREADS - 1) / THREADS;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
@@ -554,35 +557,37 @@ __device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* pre
         const int32_t n = expert_rows(p, e, &lo);
         return n / BM + (n % BM != 0);
     };
-    int32_t mine = 0;
+    int64_t mine = 0;
     for (int e = e0; e < e1; ++e)
         mine += tiles(e);
-    int32_t upto = mine;
+    int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int32_t o = __shfl_up(upto, d);
+        const int64_t o = __shfl_up((long long)upto, d);
         if ((tid & 63) >= d)
             upto += o;
     }
     if ((tid & 63) == 63)
         s_wave[tid >> 6] = upto;
     __syncthreads();
-    int32_t total = 0;
+    int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) {
         if (w < (tid >> 6))
             upto += s_wave[w];
         total += s_wave[w];
     }
-    int32_t at = upto - mine;
+    if (total > p.max_tiles)
+        return 0;
+    int32_t at = (int32_t)(upto - mine);
     for (int e = e0; e < e1; ++e) {
         prefix[e] = at;
         at += tiles(e);
     }
     if (tid == 0)
-        prefix[p.E] = total;
+        prefix[p.E] = (int32_t)total;
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(total);
+    return __builtin_amdgcn_readfirstlane((int32_t)total);
 }
 
 // x / n of the same value in every lane, x >= 0, by inv = 1 / n in fp64: off by one at most.
@@ -637,7 +642,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     static_assert(kLoadsA * 8 * kWaves == BM && kLoadsW * 8 * kWaves == BN, "loads");
     static_assert(NF % 2 == 0 && STAGES >= 2, "pairs of fragments");
     // results of a wavefront: fragments side by side, and the units they are stored in
-    constexpr int kUnit = 8192 / kWaves;
+    constexpr int kUnit = 1024;
     constexpr int kOutF = SWIGLU ? NF / 2 : NF, kUnitF = kOutF < 2 ? 1 : 2;
     constexpr int kUnitRow = kUnitF * 32 * (int)sizeof(OUT);
     constexpr int kUnitRows = kUnit / kUnitRow < 32 ? kUnit / kUnitRow : 32;
@@ -647,13 +652,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     static_assert((STAGES - 2) * kLoads + kStores <= 63, "vmcnt has six bits");
     extern __shared__ __attribute__((aligned(1024))) int8_t s_stage[];
     __shared__ __attribute__((aligned(16))) int8_t s_unit[kWaves][kUnit];
-    __shared__ int32_t s_prefix[MOE_MAX_EXPERTS + 1];
     __shared__ __attribute__((aligned(16))) float s_ws[BN];
     __shared__ float s_as[BM];
     __shared__ uint32_t s_ok[BM / 32];                        // a bit for each row to be written
     constexpr int kRing = 8;
     static_assert(STAGES + 2 <= kRing, "tiles between the loads and the products");
     __shared__ Tile s_tile[kRing];
+    int32_t* s_prefix = reinterpret_cast<int32_t*>(s_stage + STAGES * kStage);   // [E + 1]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
@@ -985,41 +990,53 @@ inline int64_t most_tiles(const MatmulArgs& p, int32_t bm)
     return p.offsets ? p.R / bm + (p.E < p.R ? p.E : p.R) : div_up(p.R, bm);
 }
 
+inline moe_status_t launched()
+{
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
 template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
-bool launch_few(MatmulArgs p, hipStream_t stream)
+moe_status_t launch_few(MatmulArgs p, hipStream_t stream)
 {
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
     const int64_t blocks = most_tiles(p, 16 * MF) * p.n_blocks;
     if (blocks * 64 * WAVES > INT32_MAX)
-        return false;
+        return MOE_ERR_UNSUPPORTED;
     k_matmul_few<MF, NF, WAVES, U, SWIGLU, OUT><<<(unsigned)blocks, 64 * WAVES, 0, stream>>>(p);
-    return true;
+    return launched();
 }
 
-// WGS: persistent workgroups of a CU; kOnce: a workgroup for each tile, taken up as CUs come free
-// (the weights of 256 experts for 4 rows each: 1190 to 1236 us against 1242 to 1253).
+// WGS: persistent workgroups of a CU; kOnce: a workgroup for each tile, taken up as CUs come free.
 constexpr int kOnce = 1 << 20;
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, int WGS, bool SWIGLU, typename OUT>
-bool launch_tile(MatmulArgs p, hipStream_t stream)
+moe_status_t launch_tile(MatmulArgs p, hipStream_t stream)
 {
-    constexpr int kThreads = 64 * WM * WN, kLds = STAGES * (BM + BN) * kStepK;
+    constexpr int kThreads = 64 * WM * WN, kStages = STAGES * (BM + BN) * kStepK;
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? BN / 2 : BN);
     p.inv_blocks = 1.0 / p.n_blocks;
     const int64_t tiles = most_tiles(p, BM) * p.n_blocks;
-    if (tiles > INT32_MAX / 2)
-        return false;
     const int64_t most = (int64_t)kCus * WGS;
     const int64_t blocks = tiles < most ? div_up(tiles, kXcds) * kXcds : most;
-    if (blocks * kThreads > INT32_MAX)
-        return false;
+    if (tiles > INT32_MAX / 2 || blocks * kThreads > INT32_MAX)
+        return MOE_ERR_UNSUPPORTED;
+    p.max_tiles = (int32_t)most_tiles(p, BM);
     const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, PIN, SWIGLU, OUT>;
-    if (kLds > 65536 && hipFuncSetAttribute((const void*)kernel,
-                                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                                            kLds) != hipSuccess)
-        return false;
-    kernel<<<(unsigned)blocks, kThreads, kLds, stream>>>(p);
-    return true;
+    if (kStages > 49152) {                                    // once a device is enough
+        static std::atomic<uint64_t> allowed{0};
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess)
+            return MOE_ERR_HIP;
+        const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+        if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+            if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    kStages + (MOE_MAX_EXPERTS + 1) * 4) != hipSuccess)
+                return MOE_ERR_HIP;
+            allowed.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
+    kernel<<<(unsigned)blocks, kThreads, kStages + (p.E + 1) * 4, stream>>>(p);
+    return launched();
 }
 
 // The tile shapes, and what a step of 128 bytes of K and a tile's beginning and end take (us, as
@@ -1068,7 +1085,7 @@ inline int choose_tile(const MatmulArgs& p, int64_t n_w)
 constexpr int64_t kFewTiles = 128;
 
 template <bool SWIGLU, typename OUT>
-bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
+moe_status_t launch_matmul(const MatmulArgs& p, hipStream_t stream)
 {
     const int64_t n_w = SWIGLU ? 2 * (int64_t)p.N : p.N;
     const int64_t experts = p.E < p.R ? p.E : p.R;
@@ -1088,8 +1105,6 @@ bool launch_matmul(const MatmulArgs& p, hipStream_t stream)
     default: return launch_tile<32, 128, 1, 2, 3, false, kOnce, SWIGLU, OUT>(p, stream);
     }
 }
-
-moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 }  // namespace
 
@@ -1151,13 +1166,12 @@ moe_status_t moe_expert_matmul_i8(const int8_t* a, const float* a_scale, int32_t
     p.N = N;
     p.K = K;
     p.n_blocks = 0;
+    p.max_tiles = 0;
     p.inv_blocks = 0.0;
     const bool bf16 = out_dtype == MOE_BF16;
-    const bool fits = act == MOE_ACT_SWIGLU ? (bf16 ? launch_matmul<true, __bf16>(p, stream)
-                                                    : launch_matmul<true, float>(p, stream))
-                                            : (bf16 ? launch_matmul<false, __bf16>(p, stream)
-                                                    : launch_matmul<false, float>(p, stream));
-    return fits ? launched() : MOE_ERR_UNSUPPORTED;
+    if (act == MOE_ACT_SWIGLU)
+        return bf16 ? launch_matmul<true, __bf16>(p, stream) : launch_matmul<true, float>(p, stream);
+    return bf16 ? launch_matmul<false, __bf16>(p, stream) : launch_matmul<false, float>(p, stream);
 }
 
 }  // extern "C"

@@ -162,6 +162,68 @@ def test_expert_matmul(T, k, E, N, K, kind, gather, act, dtype):
     check_matmul(make_matmul(T, k, E, N, K, act, gather, kind, seed=T + N), act, dtype)
 
 
+# Enough tiles for every tile shape, persistent workgroups that take several tiles, K of one step,
+# two, three and more, whole and ragged, channels that fill no block and rows of out off 16 bytes.
+TILE_SHAPES = [
+    (1100, 4, 1100, 48, "uneven", "none"), (350, 64, 520, 80, "uneven", "swiglu"),
+    (1024, 1, 2056, 2064, "even", "none"),
+    (2000, 40, 1000, 208, "uneven", "none"), (2000, 40, 996, 336, "uneven", "swiglu"),
+    (1024, 1, 4096, 1024, "even", "none"),
+    (1700, 20, 1100, 912, "uneven", "swiglu"), (2600, 40, 1100, 912, "uneven", "none"),
+    (1024, 1, 4096, 1024, "even", "swiglu"),
+    (4096, 2, 2048, 64, "uneven", "none"), (3000, 1, 2049, 144, "even", "swiglu"),
+    (9000, 2, 1536, 128, "uneven", "none"), (3000, 3, 1028, 272, "one", "swiglu"),
+    (6000, 2, 2056, 400, "uneven", "none"), (6000, 2, 1028, 400, "uneven", "swiglu"),
+    (12000, 3, 1000, 384, "uneven", "none"), (8000, 4, 602, 528, "uneven", "swiglu"),
+    (9000, 2, 2056, 656, "uneven", "none"),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,E,N,K,kind,act", TILE_SHAPES)
+def test_expert_matmul_tiles(T, E, N, K, kind, act, gather, dtype):
+    _announce(f"matmul tiles T={T} E={E} N={N} K={K} {kind} {act} gather={gather} {dtype}")
+    check_matmul(make_matmul(T, 1, E, N, K, act, gather, kind, seed=T + N + K), act, dtype)
+
+
+@pytest.mark.parametrize("T,E,N,K", [(1100, 4, 1100, 48), (2000, 40, 1000, 208),
+                                     (2600, 40, 1100, 912), (3000, 2, 2056, 144),
+                                     (12000, 3, 1000, 384)])
+def test_expert_matmul_tiles_leave_rows_they_do_not_own(T, E, N, K):
+    """Every tile shape: rows behind the last expert's, rows whose row_token is out of range, and
+    memory on both sides of out."""
+    _announce(f"matmul tiles, rows left alone T={T} E={E} N={N} K={K}")
+    m = list(make_matmul(T, 1, E, N, K, "none", True, "uneven", seed=N))
+    m[4] = np.minimum(m[4], T - T // 3).astype(np.int32)
+    m[5][[0, 3, T // 4, T - 1]] = [-1, T, 2 ** 31 - 1, -2 ** 31]
+    check_matmul(m, "none", torch.bfloat16)
+    room = torch.full((T * N + 16,), 12345.0, dtype=torch.bfloat16, device="cuda")
+    for at in (8, 1):                                    # 16-byte aligned, and 2
+        room.fill_(12345.0)
+        out = room[at:at + T * N].view(T, N)
+        a, sa, w, sw, off, rt = m
+        moe.moe_expert_matmul_i8(dev(a), dev(sa), dev(w), dev(sw), dev(off), row_token=dev(rt),
+                                 out=out)
+        want, tol, done = ref.matmul(*m, "none", True)
+        got = f64(out)
+        left = f64(torch.tensor(12345.0, dtype=torch.bfloat16))
+        assert (np.abs(got - want)[done] <= tol[done]).all() and (got[~done] == left).all()
+        assert (f64(room[:at]) == left).all() and (f64(room[at + T * N:]) == left).all()
+
+
+def test_expert_matmul_tiles_of_one_expert_without_rows_between():
+    """Experts without rows before, between and behind the ones that have them."""
+    _announce("matmul tiles, empty experts")
+    rng = np.random.default_rng(8)
+    c = np.zeros(200, np.int64)
+    c[[3, 4, 70, 131, 199]] = [500, 1, 129, 900, 257]
+    m = list(make_matmul(int(c.sum()), 1, 200, 136, 160, "none", True, "even", seed=8))
+    m[4] = np.concatenate([[0], np.cumsum(c)]).astype(np.int32)
+    m[5] = rng.permutation(int(c.sum())).astype(np.int32)
+    check_matmul(m, "none", torch.float32)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 4096, 7168), (5, 70, 96), (260, 300, 336)])
 def test_plain_product(T, N, K):
     _announce(f"matmul without offsets T={T} N={N} K={K}")
@@ -392,6 +454,60 @@ def test_router_training_step():
     logits, _, mask, _, dw = make_balance(240, 3, 48, 4, True, seed=21)
     idx, wt = moe.moe_route_topk(dev(logits), 4)
     check_balance(logits, to_host(idx), mask, to_host(wt), dw, 3, 0.02)
+
+
+def test_expert_layer_of_one_rank_after_receive():
+    """The rows that a rank received from two sources: 8-bit rows and both products up to the rows
+    received (expert_offsets of moe_ep_recv), nothing behind them."""
+    _announce("expert layer after moe_ep_recv")
+    S, T, E, k, N, H, inner = 2, 160, 16, 4, 2, 256, 128
+    L, cap = E // N, T * 4
+    rng = np.random.default_rng(5)
+    regions = torch.zeros((N * S * cap, H), dtype=torch.bfloat16, device="cuda")
+    counts = torch.zeros((N, S, L), dtype=torch.int32, device="cuda")
+    for s in range(S):
+        x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16)
+        idx, _ = moe.moe_route_topk(dev(rng.standard_normal((T, E)).astype(np.float32)), k)
+        moe.moe_ep_send(x.cuda(), idx, E, N, s, S, cap, regions, counts,
+                        torch.empty(T * k, dtype=torch.int32, device="cuda"),
+                        moe.alloc_workspace(T, E, k))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    grouped = torch.zeros((S * cap, H), dtype=torch.bfloat16, device="cuda")
+    off, src = torch.empty(L + 1, **i32), torch.empty(S * cap, **i32)
+    moe.moe_ep_recv(regions, E, N, 1, S, cap, counts, grouped, torch.empty(L, **i32), off, src)
+    _, _, w1, s1, w2, s2 = make_layer(1, 1, L, H, inner, seed=9)
+    n = int(off[L])
+    assert 0 < n < S * cap
+    q = torch.full((S * cap, H), 9, dtype=torch.int8, device="cuda")
+    sx = torch.full((S * cap,), -1.0, device="cuda")
+    moe.moe_quant_rows(grouped, q=q, scale=sx, n_rows=off[L:])
+    h = torch.full((S * cap, inner), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_matmul_i8(q, sx, dev(w1), dev(s1), off, act="swiglu", out=h)
+    assert (to_host(q)[n:] == 9).all() and (f64(sx)[n:] == -1.0).all() and (f64(h)[n:] == 7.0).all()
+    want_q, want_s = ref.quant(f64(grouped)[:n])
+    assert np.array_equal(to_host(q)[:n], want_q) and np.array_equal(to_host(sx)[:n], want_s)
+    want, tol, done = ref.matmul(to_host(q), to_host(sx), w1, s1, to_host(off), None, "swiglu", True)
+    assert done[:n].all() and not done[n:].any() and (np.abs(f64(h) - want)[:n] <= tol[:n]).all()
+
+
+@pytest.mark.parametrize("T,E,N,K", [(2000, 40, 1000, 208), (2600, 40, 1100, 912),
+                                     (12000, 3, 1000, 384)])
+def test_tiles_in_a_graph(T, E, N, K):
+    """The tile shapes that take more LDS than a launch has by default, first used in a capture."""
+    _announce(f"tiles in a graph T={T} E={E} N={N} K={K}")
+    m = make_matmul(T, 1, E, N, K, "none", False, "uneven", seed=3)
+    a, sa, w, sw, off = [dev(v) for v in m[:5]]
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_expert_matmul_i8(a, sa, w, sw, off, out=out)
+    want = moe.moe_expert_matmul_i8(a, sa, w, sw, off)
+    for rep in range(4):
+        out.fill_(-1.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), rep
 
 
 def test_expert_layer_and_router_step_in_a_graph():
