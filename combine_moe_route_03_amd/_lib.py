@@ -422,6 +422,19 @@ def _matrix(name: str, t: torch.Tensor) -> torch.device:
     return t.device
 
 
+def _empty(shape, dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's pool: what was freed on another stream may
+    still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = (torch.cuda.ExternalStream(raw, device=device) if raw
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 _MASKS = (torch.bool, torch.uint8)
 _WIDE = (torch.bfloat16, torch.float32)
 
@@ -470,19 +483,16 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     if n_seqs < 1 or T % n_seqs:
         raise ValueError(f"n_seqs: {n_seqs} sequences do not divide {T} tokens")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        loss = _empty((1,), torch.float32, dev, stream)
     if expert_counts is None:
-        expert_counts = torch.empty((n_seqs, E), dtype=torch.int32, device=dev)
+        expert_counts = _empty((n_seqs, E), torch.int32, dev, stream)
     if prob_sums is None:
-        prob_sums = torch.empty((n_seqs, E), dtype=torch.float32, device=dev)
+        prob_sums = _empty((n_seqs, E), torch.float32, dev, stream)
     if seq_tokens is None:
-        seq_tokens = torch.empty(n_seqs, dtype=torch.int32, device=dev)
+        seq_tokens = _empty((n_seqs,), torch.int32, dev, stream)
     if workspace is None:
-        workspace = alloc_balance_workspace(T, E, n_seqs, dev)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
-        elif stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=dev))
+        workspace = _empty((max(moe_balance_workspace_bytes(T, E, n_seqs), 1),), torch.uint8, dev,
+                           stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: needs contiguous memory on {dev}")
     _enqueue("moe_balance_loss", dev, stream,
@@ -511,7 +521,7 @@ def moe_route_grad(logits: torch.Tensor, topk_idx: torch.Tensor,
     k = topk_idx.shape[-1]
     n_seqs = int(n_seqs)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dlogits = _empty((T, E), torch.float32, dev, stream)
     _enqueue("moe_route_grad", dev, stream,
              _arg("logits", logits, torch.float32, (T, E), dev),
              _arg("topk_idx", topk_idx, torch.int32, (T, k), dev),
@@ -533,9 +543,9 @@ def moe_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     dev = _matrix("x", x)
     R, H = x.shape
     if q is None:
-        q = torch.empty((R, H), dtype=torch.int8, device=dev)
+        q = _empty((R, H), torch.int8, dev, stream)
     if scale is None:
-        scale = torch.empty(R, dtype=torch.float32, device=dev)
+        scale = _empty((R,), torch.float32, dev, stream)
     _enqueue("moe_quant_rows", dev, stream, _arg("x", x, _WIDE, (R, H), dev), _dtype_code(x), R, H,
              _opt("n_rows", n_rows, torch.int32, (1,), dev), _arg("q", q, torch.int8, (R, H), dev),
              _arg("scale", scale, torch.float32, (R,), dev))
@@ -563,7 +573,7 @@ def moe_expert_matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor
     N = n_w // 2 if act == "swiglu" else n_w
     R = A if row_token is None else row_token.numel()
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        out = _empty((R, N), out_dtype, dev, stream)
     _enqueue("moe_expert_matmul_i8", dev, stream, _arg("a", a, torch.int8, (A, K), dev),
              _arg("a_scale", a_scale, torch.float32, (A,), dev), A,
              _opt("row_token", row_token, torch.int32, (R,), dev),

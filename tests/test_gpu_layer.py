@@ -175,7 +175,7 @@ TILE_SHAPES = [
     (9000, 2, 1536, 128, "uneven", "none"), (3000, 3, 1028, 272, "one", "swiglu"),
     (6000, 2, 2056, 400, "uneven", "none"), (6000, 2, 1028, 400, "uneven", "swiglu"),
     (12000, 3, 1000, 384, "uneven", "none"), (8000, 4, 602, 528, "uneven", "swiglu"),
-    (9000, 2, 2056, 656, "uneven", "none"),
+    (4000, 1, 2056, 272, "even", "swiglu"), (6000, 2, 4100, 400, "uneven", "none"),
 ]
 
 
