@@ -969,25 +969,35 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
                             }
                     }
                     asm volatile("" ::: "memory");
+                    const auto at16 = [&](int r, int c) {     // piece c of row r
+                        return unit + r * kUnitRow + (c ^ (r & (kPieces - 1) & 7)) * 16;
+                    };
+                    const int32_t n1 = n0 + (wn * kOutF + u) * 32;
+                    const int32_t tr0 = (wm * MF + m) * 32 + phase * kUnitRows;
+                    const uint32_t ok_rows = rows >> phase * kUnitRows;
+                    if (wide) {
 #pragma unroll
-                    for (int s = 0; s < kUnitStores; ++s) {
-                        const int r = s * (kUnitRows / kUnitStores) + lane / kPieces;
-                        const int c = lane % kPieces;
-                        const int rr = phase * kUnitRows + r;
-                        const u32x4 out = *reinterpret_cast<const u32x4*>(
-                            unit + r * kUnitRow + (c ^ (r & (kPieces - 1) & 7)) * 16);
-                        const int32_t n = n0 + (wn * kOutF + u) * 32 + c * (16 / (int)sizeof(OUT));
-                        const int32_t tr = (wm * MF + m) * 32 + rr;
-                        const bool write = (rows >> rr & 1) && n < p.N;
-                        if (wide) {
-                            store_buffer(out, obuf, write ? (uint32_t)(tr * p.N + n) * (uint32_t)sizeof(OUT)
-                                                        : 0xFFFFFFF0u);
-                        } else if (write) {
-                            const OUT* x = reinterpret_cast<const OUT*>(
-                                unit + r * kUnitRow + (c ^ (r & (kPieces - 1) & 7)) * 16);
-                            const int left = min(16 / (int)sizeof(OUT), p.N - n);
-                            for (int i = 0; i < left; ++i)
-                                base[(int64_t)tr * p.N + n + i] = x[i];
+                        for (int s = 0; s < kUnitStores; ++s) {
+                            const int r = s * (kUnitRows / kUnitStores) + lane / kPieces;
+                            const int c = lane % kPieces;
+                            const u32x4 out = *reinterpret_cast<const u32x4*>(at16(r, c));
+                            const int32_t n = n1 + c * (16 / (int)sizeof(OUT));
+                            const uint32_t to = (uint32_t)((tr0 + r) * p.N + n) *
+                                                (uint32_t)sizeof(OUT);
+                            store_buffer(out, obuf,
+                                         (ok_rows >> r & 1) && n < p.N ? to : 0xFFFFFFF0u);
+                        }
+                    } else {                                  // a value a lane, side by side
+                        constexpr int kCols = kUnitF * 32;
+                        constexpr int kUnroll = sizeof(OUT) == 2 ? 4 : 1;   // (registers)
+#pragma unroll kUnroll
+                        for (int s = 0; s < kUnitRows * kCols / 64; ++s) {
+                            const int r = s * (64 / kCols) + lane / kCols, c = lane % kCols;
+                            const int byte = c * (int)sizeof(OUT);
+                            const OUT out = *reinterpret_cast<const OUT*>(at16(r, byte / 16) +
+                                                                          byte % 16);
+                            if ((ok_rows >> r & 1) && n1 + c < p.N)
+                                base[(int64_t)(tr0 + r) * p.N + n1 + c] = out;
                         }
                     }
                 }
