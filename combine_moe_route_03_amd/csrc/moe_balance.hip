@@ -20,8 +20,8 @@ constexpr int kGradThreads = 256;
 constexpr int kMaxLossBlocks = 512;      // workgroups of the forward pass, two a CU
 constexpr int kLossTokens = 32;          //   of no fewer tokens than two a wavefront
 constexpr int kDirectTokens = 192;       // one workgroup and one launch up to so many tokens
-constexpr int kFinishExperts = 64;       // experts of a finishing workgroup
-constexpr int kFinishThreads = 512;      //   by 8 slices of the partial sums
+constexpr int kFinishExperts = 32;       // experts of a finishing workgroup
+constexpr int kFinishThreads = 512;      //   by 16 slices of the partial sums
 constexpr int kFinishSlices = kFinishThreads / kFinishExperts;
 
 // A row of E fp32 values over the G lanes of a group: lane g holds elements (v * G + g) * VEC + c.
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(kLossThreads) void k_balance_partial(LossArgs a)
     for (int i = 0; i < NV * VEC; ++i)
         sum.v[i] = 0.0f;
     int seen = 0;
-    constexpr int U = NV * VEC <= 4 ? 4 : NV * VEC <= 8 ? 2 : 1;      // rows in flight
+    // rows in flight; two workgroups a CU leave 64 registers
+    constexpr int U = (DIRECT ? 2 : 1) * (NV * VEC <= 4 ? 4 : NV * VEC <= 8 ? 2 : 1);
     for (int t0 = grp; t0 < n; t0 += U * kGroups) {
         Row<G, NV, VEC> r[U];
         bool use[U];
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(kLossThreads) void k_balance_partial(LossArgs a)
     }
 }
 
-// Sums the workgroups' parts of 64 experts of one sequence (8 slices side by side, joined in
+// Sums the workgroups' parts of 32 experts of one sequence (16 slices side by side, joined in
 // order, fp64) and its share of the loss; the last workgroup to finish adds the shares up in their
 // order. The shares cross XCDs, whose L2s are not coherent, so they are stored and loaded at
 // device scope.
@@ -260,39 +261,37 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(LossArgs a, i
     const int tid = threadIdx.x;
     const int s = blockIdx.x / eb, c = blockIdx.x % eb;
     const int e = c * kFinishExperts + tid % kFinishExperts, slice = tid / kFinishExperts;
+    int32_t tokens = 0;
+    for (int b = tid; b < a.nb; b += kFinishThreads)
+        tokens += a.part_tokens[(int64_t)s * a.nb + b];
     if (tid == 0)
         s_tokens = 0;
-    __syncthreads();
     double p = 0.0;
     int32_t n = 0;
     if (e < a.E) {
         const float* sum = a.part_sum + (int64_t)s * a.nb * a.E + e;
         const int32_t* count = a.part_count + (int64_t)s * a.nb * a.E + e;
-        int b = slice;
-        for (; b + 3 * kFinishSlices < a.nb; b += 4 * kFinishSlices) {
-            float x[4];
-            int32_t c[4];
+        // eight parts in flight: up to 128 of them take one round
+        for (int b0 = slice; b0 < a.nb; b0 += 8 * kFinishSlices) {
+            float x[8];
+            int32_t c[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = sum[(int64_t)(b + i * kFinishSlices) * a.E];
-                c[i] = count[(int64_t)(b + i * kFinishSlices) * a.E];
+            for (int i = 0; i < 8; ++i) {
+                const int64_t at = (int64_t)min(b0 + i * kFinishSlices, a.nb - 1) * a.E;
+                x[i] = sum[at];
+                c[i] = count[at];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p += x[i];
-                n += c[i];
-            }
-        }
-        for (; b < a.nb; b += kFinishSlices) {
-            p += sum[(int64_t)b * a.E];
-            n += count[(int64_t)b * a.E];
+            for (int i = 0; i < 8; ++i)
+                if (b0 + i * kFinishSlices < a.nb) {
+                    p += x[i];
+                    n += c[i];
+                }
         }
     }
     s_sum[tid] = p;
     s_count[tid] = n;
-    int32_t tokens = 0;
-    for (int b = tid; b < a.nb; b += kFinishThreads)
-        tokens += a.part_tokens[(int64_t)s * a.nb + b];
+    __syncthreads();
     if (tokens)
         atomicAdd(&s_tokens, tokens);
     __syncthreads();
