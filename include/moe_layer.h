@@ -36,8 +36,8 @@ extern "C" {
  *   seq_tokens    [S] int32 out: n_s. Counts and tokens are what moe_route_grad takes.
  *   workspace     moe_balance_workspace_bytes(T, E, S) bytes, 16-byte aligned, any contents; calls
  *                 that may run at the same time must not share one.
- * p, the sums of a workgroup and the loss's terms are fp32, sums over workgroups fp64; every order
- * is fixed, so equal inputs give equal bits. Requires T % S == 0, T * k < 2^31, 1 <= S, E, k (else
+ * p and the sums of a workgroup are fp32, sums over workgroups and the loss fp64; every order is
+ * fixed, so equal inputs give equal bits. Requires T % S == 0, T * k < 2^31, 1 <= S, E, k (else
  * MOE_ERR_INVALID), S <= MOE_MAX_SEQS, E <= MOE_MAX_EXPERTS and k <= MOE_MAX_TOPK (else
  * MOE_ERR_UNSUPPORTED). T = 0 writes zeros.
  */
