@@ -593,6 +593,103 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(g, w))
 
 
+# --------------------------------------------------------------- offsets beyond 32 bits --
+def big(*shape):
+    """Random 8-bit values, without a copy of them in a wider type."""
+    out = torch.empty(shape, dtype=torch.int8, device="cuda")
+    flat = out.view(-1)
+    g = torch.Generator(device="cuda").manual_seed(len(flat) % 1000)
+    for i in range(0, flat.numel(), 1 << 28):
+        flat[i:i + (1 << 28)].random_(-127, 128, generator=g)
+    return out
+
+
+def test_quant_rows_beyond_2_31_elements():
+    _announce("quant_rows beyond 2^31 elements")
+    R, H = 300000, 8192
+    x = torch.empty((R, H), dtype=torch.bfloat16, device="cuda").normal_()
+    q, s = moe.moe_quant_rows(x)
+    rows = [0, 1, R // 2, 2 ** 31 // H - 1, 2 ** 31 // H, R - 2, R - 1]
+    want_q, want_s = ref.quant(f64(x[rows]))
+    assert np.array_equal(to_host(q[rows]), want_q) and np.array_equal(to_host(s[rows]), want_s)
+
+
+@pytest.mark.parametrize("R", [40, 700])
+def test_expert_matmul_rows_and_weights_beyond_2_31_bytes(R):
+    """Rows gathered from 2.5 GB, and an expert's weights of 2.5 GB, by few rows and by tiles."""
+    _announce(f"matmul beyond 2^31 bytes R={R}")
+    K, big_n = 8192, 300000
+    rng = np.random.default_rng(1)
+    a = big(big_n, K)
+    rt = rng.integers(0, big_n, R).astype(np.int32)
+    rt[:4] = [0, big_n - 1, 2 ** 31 // K, 2 ** 31 // K - 1]
+    w = big(2, 264, K)
+    sa, sw = torch.rand(big_n, device="cuda"), torch.rand((2, 264), device="cuda") / 1e5
+    off = np.array([0, R // 3, R], np.int32)
+    got = f64(moe.moe_expert_matmul_i8(a, sa, w, sw, dev(off), row_token=dev(rt),
+                                       out_dtype=torch.float32))
+    small = a[dev(rt).long()]
+    want, tol, _ = ref.matmul(to_host(small), to_host(sa[dev(rt).long()]), to_host(w), to_host(sw),
+                              off, None, "none", False)
+    assert (np.abs(got - want) <= tol).all()
+    del a
+    w = big(2, big_n, K)
+    sw = torch.rand((2, big_n), device="cuda") / 1e5
+    x, sx = small, torch.rand(R, device="cuda")
+    got = moe.moe_expert_matmul_i8(x, sx, w, sw, dev(off), out_dtype=torch.float32)
+    cols = [0, 1, 2 ** 31 // K - 1, 2 ** 31 // K, big_n - 2, big_n - 1]
+    want, tol, _ = ref.matmul(to_host(x), to_host(sx), to_host(w[:, cols].contiguous()),
+                              to_host(sw[:, cols].contiguous()), off, None, "none", False)
+    assert (np.abs(f64(got[:, cols]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("N", [40000, 40001])
+def test_expert_matmul_results_beyond_2_31_elements(N):
+    _announce(f"matmul results beyond 2^31 elements N={N}")
+    R, K = 60000, 32
+    a, w = big(R, K), big(3, N, K)
+    sa, sw = torch.rand(R, device="cuda"), torch.rand((3, N), device="cuda")
+    off = np.array([0, 100, 50000, R], np.int32)
+    got = moe.moe_expert_matmul_i8(a, sa, w, sw, dev(off))
+    rows = np.array([0, 99, 100, 49999, 50000, 2 ** 31 // N - 1, 2 ** 31 // N, 2 ** 31 // N + 1,
+                     R - 1])
+    for e in range(3):
+        r = rows[(rows >= off[e]) & (rows < off[e + 1])]
+        d = dev(r)
+        want, tol, _ = ref.matmul(to_host(a[d]), to_host(sa[d]), to_host(w[e:e + 1]),
+                                  to_host(sw[e:e + 1]), [0, len(r)], None, "none", True)
+        assert (np.abs(f64(got[d]) - want) <= tol).all()
+
+
+def test_balance_beyond_2_31_logits():
+    _announce("balance beyond 2^31 logits")
+    T, E, k, S = 2200000, 1024, 2, 2
+    logits = torch.empty((T, E), device="cuda").normal_()
+    idx = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+    loss, counts, sums, tokens = moe.moe_balance_loss(logits, idx, 0.01, n_seqs=S)
+    assert to_host(tokens).tolist() == [T // S] * S
+    for s in range(S):
+        part = slice(s * (T // S), (s + 1) * (T // S))
+        assert torch.equal(counts[s].long(), torch.bincount(idx[part].reshape(-1).long(), minlength=E))
+        want = torch.zeros(E, dtype=torch.float64, device="cuda")
+        for c in logits[part].split(1 << 17):
+            want += torch.softmax(c.double(), 1).sum(0)
+        # the additions of a workgroup's chain: its share of the tokens, and the probabilities' 50u
+        assert ((sums[s] - want).abs() <= (T / S / 256 / 16 + 150) * ref.U * want).all()
+    d = moe.moe_route_grad(logits, idx, expert_counts=counts, seq_tokens=tokens, alpha=0.01,
+                           n_seqs=S)
+    rows = [0, T // S - 1, T // S, 2 ** 31 // E - 1, 2 ** 31 // E, T - 1]
+    l64, c64 = f64(logits[rows]), f64(counts)
+    p = ref.probs(l64)
+    for i, t in enumerate(rows):
+        s = t // (T // S)
+        c = c64[s] - float(round(k * (T // S) / E))
+        f = 0.01 / S * E / (k * float(T // S) ** 2)
+        want = f * p[i] * (c - (c * p[i]).sum())
+        tol = f * p[i] * (np.abs(c - (c * p[i]).sum()) + (np.abs(c) * p[i]).sum()) * 80 * ref.U
+        assert (np.abs(f64(d[t]) - want) <= tol + 2.0 ** -120).all()
+
+
 def test_binding_refusals_on_the_gpu():
     _announce("binding refusals")
     x = torch.zeros((4, 32), device="cuda")
