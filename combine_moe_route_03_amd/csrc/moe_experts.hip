@@ -6,7 +6,7 @@
 //                  it (128 tokens over 256 experts: 7.5 GB in 1.19 ms, 6.3 TB/s), with many the
 //                  matrix cores and the LDS that feeds them (8192^3: 2.3 to 2.4 POPS).
 //   k_matmul_few   the same where there are too few tiles to fill the GPU: the wavefronts of a
-//                  workgroup share K (one row by 29 MB of weights: 8.7 us).
+//                  workgroup share K (one row by 29 MB of weights: 7.7 us).
 #include <atomic>
 
 #include "moe_device.h"
@@ -327,9 +327,13 @@ template <int BM>
 __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t index)
 {
     const int lane = threadIdx.x & 63;
+    int32_t mine = 0, lo = 0;
+    if (p.E == 1) {
+        const int32_t rows = expert_rows(p, 0, &lo);
+        return Tile{0, lo + index * BM, max(0, min(BM, rows - index * BM)), 0};
+    }
     const int per = (p.E + 63) / 64;
     const int e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
-    int32_t mine = 0, lo = 0;
     for (int e = e0; e < e1; ++e)
         mine += (expert_rows(p, e, &lo) + BM - 1) / BM;
     int32_t upto = mine;
@@ -418,6 +422,28 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
         src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
         ap[m] = p.a + (int64_t)src * p.K;
     }
+    // the fragment (with SwiGLU the pair) that this wavefront will join and store: its scales are
+    // read ahead
+    constexpr int kStep = SWIGLU ? 2 : 1;
+    static_assert(kFrags <= WAVES * kStep, "one for a wavefront");
+    const int mine = wave * kStep;
+    const int32_t at_row = 16 * (mine / NF) + r16;
+    const int32_t row = tile.row0 + min(at_row, tile.rows - 1);
+    const int32_t src = p.row_token ? p.row_token[row] : row;
+    const int32_t n = n0 + (SWIGLU ? 8 : 16) * (mine % NF) + 4 * kq;
+    const int32_t left = p.N - n;
+    const bool stores = mine < kFrags && at_row < tile.rows &&
+                        (uint32_t)src < (uint32_t)p.a_rows && left > 0;
+    float sa = 0.0f, sw[4], su[4];
+    if (stores) {
+        const float* s = p.w_scale + (int64_t)tile.e * n_w + n;
+        sa = p.a_scale[src];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            sw[c] = s[c < left ? c : 0];
+            su[c] = SWIGLU ? s[p.N + (c < left ? c : 0)] : 0.0f;
+        }
+    }
     i32x4 acc[MF][NF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -457,48 +483,33 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
         for (int f = 0; f < NF; ++f)
             s_acc[wave][m * NF + f][lane] = acc[m][f];
     __syncthreads();
-    constexpr int kStep = SWIGLU ? 2 : 1;
-    for (int i = wave * kStep; i < kFrags; i += WAVES * kStep) {
-        const int m = i / NF, f = i % NF;
-        i32x4 sum[2];
+    if (!stores)
+        return;
+    i32x4 sum[2];
 #pragma unroll
-        for (int g = 0; g < kStep; ++g) {
-            sum[g] = s_acc[0][i + g][lane];
+    for (int g = 0; g < kStep; ++g) {
+        sum[g] = s_acc[0][mine + g][lane];
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w)
-                sum[g] += s_acc[w][i + g][lane];
-        }
-        const int32_t at = 16 * m + r16;
-        const int32_t r = tile.row0 + min(at, tile.rows - 1);
-        const int32_t src = p.row_token ? p.row_token[r] : r;
-        const int32_t n = n0 + (SWIGLU ? 8 : 16) * f + 4 * kq;
-        const int32_t left = p.N - n;
-        if (at >= tile.rows || (uint32_t)src >= (uint32_t)p.a_rows || left <= 0)
-            continue;
-        const float sa = p.a_scale[src];
-        const float* sw = p.w_scale + (int64_t)tile.e * n_w + n;
-        OUT* out = static_cast<OUT*>(p.out) + (int64_t)r * p.N + n;
-        float v[4];
+        for (int w = 1; w < WAVES; ++w)
+            sum[g] += s_acc[w][mine + g][lane];
+    }
+    OUT* out = static_cast<OUT*>(p.out) + (int64_t)row * p.N + n;
+    typedef typename Four<OUT>::type four;
+    four v;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int o = c < left ? c : 0;
-            v[c] = (float)sum[0][c] * sa * sw[o];
-            if (SWIGLU)
-                v[c] = swiglu(v[c], (float)sum[kStep - 1][c] * sa * sw[p.N + o]);
-        }
-        typedef typename Four<OUT>::type four;
-        if (left >= 4 && (uintptr_t)out % sizeof(four) == 0) {
-            four x;
+    for (int c = 0; c < 4; ++c) {
+        float y = (float)sum[0][c] * sa * sw[c];
+        if (SWIGLU)
+            y = swiglu(y, (float)sum[kStep - 1][c] * sa * su[c]);
+        v[c] = (OUT)y;
+    }
+    if (left >= 4 && (uintptr_t)out % sizeof(four) == 0) {
+        *reinterpret_cast<four*>(out) = v;
+    } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                x[c] = (OUT)v[c];
-            *reinterpret_cast<four*>(out) = x;
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < left)
-                    out[c] = (OUT)v[c];
-        }
+        for (int c = 0; c < 4; ++c)
+            if (c < left)
+                out[c] = v[c];
     }
 }
 
@@ -1104,7 +1115,7 @@ inline int choose_tile(const MatmulArgs& p, int64_t n_w)
 
 // Few tiles leave most of the GPU idle and their K axis in one workgroup: there the wavefronts of a
 // workgroup share K, and 16 or 32 channels make a workgroup (one row by 4096 channels, K = 7168:
-// 8.7 us against 28; 64 rows: 19 against 28; 128 rows, 128 tiles of 32 x 128: 33 against 28).
+// 7.7 us against 28; 64 rows: 17 against 28; 128 rows, 128 tiles of 32 x 128: 32 against 28).
 constexpr int64_t kFewTiles = 128;
 
 template <bool SWIGLU, typename OUT>
@@ -1115,10 +1126,10 @@ moe_status_t launch_matmul(const MatmulArgs& p, hipStream_t stream)
     const int64_t rows = div_up(p.R, experts);
     if (most_tiles(p, 32) * div_up(n_w, 128) < kFewTiles) {
         if (rows > 16)
-            return launch_few<2, 2, 8, 2, SWIGLU, OUT>(p, stream);
+            return launch_few<2, 2, 8, 4, SWIGLU, OUT>(p, stream);
         if (SWIGLU || most_tiles(p, 16) * div_up(n_w, 16) > 512)
             return launch_few<1, 2, 8, 4, SWIGLU, OUT>(p, stream);
-        return launch_few<1, SWIGLU ? 2 : 1, 8, 4, SWIGLU, OUT>(p, stream);
+        return launch_few<1, SWIGLU ? 2 : 1, 8, SWIGLU ? 4 : 2, SWIGLU, OUT>(p, stream);
     }
     switch (choose_tile(p, n_w)) {
     case 0: return launch_tile<256, 256, 2, 4, 2, true, 1, SWIGLU, OUT>(p, stream);
