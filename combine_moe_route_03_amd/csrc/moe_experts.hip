@@ -1050,10 +1050,12 @@ moe_status_t launch_tile(MatmulArgs p, hipStream_t stream)
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? BN / 2 : BN);
     p.inv_blocks = 1.0 / p.n_blocks;
     const int64_t tiles = most_tiles(p, BM) * p.n_blocks;
-    const int64_t most = (int64_t)kCus * WGS;
-    const int64_t blocks = tiles < most ? div_up(tiles, kXcds) * kXcds : most;
-    if (tiles > INT32_MAX / 2 || blocks * kThreads > INT32_MAX)
+    if (tiles > INT32_MAX / 2)
         return MOE_ERR_UNSUPPORTED;
+    int64_t most = (int64_t)kCus * WGS;                       // and below 2^31 threads
+    if (most > INT32_MAX / kThreads / kXcds * kXcds)
+        most = INT32_MAX / kThreads / kXcds * kXcds;
+    const int64_t blocks = tiles < most ? div_up(tiles, kXcds) * kXcds : most;
     p.max_tiles = (int32_t)most_tiles(p, BM);
     const auto kernel = k_matmul_tile<BM, BN, WM, WN, STAGES, PIN, SWIGLU, OUT>;
     if (kStages > 49152) {                                    // once a device is enough
