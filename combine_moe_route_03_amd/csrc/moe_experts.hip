@@ -363,14 +363,16 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t index)
 
 // gate / (1 + exp(-gate)) * up, with exp(x) = 2^(x log2 e): the product's rounding, |gate| 2^-24
 // of the result, is added back to first order; v_exp_f32 and v_rcp_f32 are good to one ulp. Beyond
-// 2^126 (the quotient is below 2^-119 then) exp goes without, so that infinity stays one.
+// 2^126 (the quotient is below 2^-119 then) and below 2^-126 (next to 1 nothing is left of it) exp
+// goes without: the rest of an infinite t is infinite or NaN, also for finite gates from 2.36e38.
 __device__ __forceinline__ float swiglu(float gate, float up)
 {
     constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
     const float t = gate * hi;
     const float rest = __builtin_fmaf(gate, hi, -t) + gate * lo;
     const float e = __builtin_amdgcn_exp2f(t);
-    const float s = 1.0f + (t > 126.0f ? e : __builtin_fmaf(e, rest * 0.693147182f, e));
+    const float s = 1.0f + (__builtin_fabsf(t) > 126.0f ? e
+                                                          : __builtin_fmaf(e, rest * 0.693147182f, e));
     return gate * __builtin_amdgcn_rcpf(s) * up;
 }
 

@@ -262,6 +262,49 @@ def test_expert_matmul_nan_scale_reaches_its_rows_only():
     assert np.isnan(got[rows]).all() and np.isfinite(got[~rows]).all()
 
 
+GATES = [0.5, 20.0, 43.0, 64.1, 87.5, 88.5, 90.0, 133.0, 1e3, 1e30, 2.3e38, 2.36e38, 2.4e38, 3.4e38,
+         np.inf, -0.5, -20.0, -43.0, -1e3, -1e30, -2.3e38, -2.36e38, -2.4e38, -3.4e38, -np.inf]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,N,E,K", [(60, 40, 8, 16), (60, 40, 1, 160), (104, 264, 30, 144),
+                                     (2000, 996, 40, 336), (3000, 2049, 1, 16),
+                                     (9000, 1032, 4, 1424), (6000, 1028, 2, 400),
+                                     (4000, 2056, 1, 272)])
+def test_expert_matmul_swiglu_over_the_range_of_gates(R, N, E, K, dtype):
+    """silu(gate) * up for gates of both signs from 0.5 to infinity, by few rows and by tiles. A row
+    has |gate| as its scale and the gate's sign in its first code, so that y is exactly the fp32
+    product of scales: the gate is row scale times 1 or 2, up is row scale times 2^-130 to 1e30.
+    Off by exp 3u, 1 + exp u, reciprocal 2u and two products: 8u, taken as 16u; by what silu loses
+    below 2^-126, four halves of its last place 2^-149, times up; by a result below 2^-126, which
+    may be flushed; and by the last rounding."""
+    _announce(f"matmul gates R={R} N={N} E={E} K={K} {dtype}")
+    gates = np.array(GATES)[np.arange(R) * 7 % len(GATES)]
+    a = np.zeros((R, K), np.int8)
+    a[:, 0], a[:, 1] = np.sign(gates), 1
+    w = np.zeros((E, 2 * N, K), np.int8)
+    w[:, :N, 0], w[:, N:, 1] = 1, 1
+    sa = np.abs(gates).astype(np.float32)
+    sw = np.empty((E, 2 * N), np.float32)
+    sw[:, :N] = np.array([1.0, 2.0], np.float32)[np.arange(N) // 4 % 2]
+    sw[:, N:] = np.array([1.0, 1e-3, 1e30, 2.0 ** -130], np.float32)[np.arange(N) % 4]
+    off = (np.arange(E + 1) * R // E).astype(np.int32)
+    got = f64(run_matmul((a, sa, w, sw, off, None), "swiglu", dtype))
+    u, half = ref.U, torch.finfo(dtype).eps / 2
+    with np.errstate(all="ignore"):
+        gate = ((a[:, :1] * sa[:, None]) * sw[0, :N]).astype(np.float64)
+        up = (sa[:, None] * sw[0, N:]).astype(np.float64)
+        want = ref.silu(gate) * up
+        tol = np.abs(want) * (16 * u + half) + np.abs(up) * 4 * 2.0 ** -150 + 2.0 ** -126
+        top = f64(torch.from_numpy(want).to(dtype))              # what the type cannot hold
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        inf = np.isinf(top)
+        assert np.array_equal(got[inf], top[inf])
+        rest = np.isfinite(top)
+        bad = np.abs(got - want)[rest] > tol[rest]
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, gates {np.unique(gate[rest][bad])}"
+
+
 def test_expert_matmul_empty():
     _announce("matmul empty")
     m = make_matmul(4, 1, 4, 64, 128, "none", False, "one")
