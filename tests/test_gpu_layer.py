@@ -263,7 +263,9 @@ def test_expert_matmul_nan_scale_reaches_its_rows_only():
 
 
 GATES = [0.5, 20.0, 43.0, 64.1, 87.5, 88.5, 90.0, 133.0, 1e3, 1e30, 2.3e38, 2.36e38, 2.4e38, 3.4e38,
-         np.inf, -0.5, -20.0, -43.0, -1e3, -1e30, -2.3e38, -2.36e38, -2.4e38, -3.4e38, -np.inf]
+         np.inf, -0.5, -20.0, -43.0, -1e3, -1e30, -2.3e38, -2.36e38, -2.4e38, -3.4e38, -np.inf,
+         -44.0, -45.0, -50.0, -63.9, -64.1, -66.0, -67.0, -87.0, -87.5, -88.0, -88.5, -89.0, -90.0,
+         -92.0, -95.0, -100.0, -110.0, -133.0, -178.0]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -275,7 +277,8 @@ def test_expert_matmul_swiglu_over_the_range_of_gates(R, N, E, K, dtype):
     """silu(gate) * up for gates of both signs from 0.5 to infinity, by few rows and by tiles. A row
     has |gate| as its scale and the gate's sign in its first code, so that y is exactly the fp32
     product of scales: the gate is row scale times 1 or 2, up is row scale times 2^-130 to 1e30.
-    Off by exp 3u, 1 + exp u, reciprocal 2u and two products: 8u, taken as 16u; by what silu loses
+    Off by exp 3u, 1 + exp u, reciprocal 2u (far below zero two reciprocals of sqrt(exp), 5u each)
+    and two or three products: 13u at most, taken as 16u for the second order; by what silu loses
     below 2^-126, four halves of its last place 2^-149, times up; by a result below 2^-126, which
     may be flushed; and by the last rounding."""
     _announce(f"matmul gates R={R} N={N} E={E} K={K} {dtype}")
@@ -303,6 +306,19 @@ def test_expert_matmul_swiglu_over_the_range_of_gates(R, N, E, K, dtype):
         rest = np.isfinite(top)
         bad = np.abs(got - want)[rest] > tol[rest]
     assert not bad.any(), f"{bad.sum()} of {bad.size} off, gates {np.unique(gate[rest][bad])}"
+
+
+def test_expert_matmul_swiglu_of_a_row_does_not_depend_on_its_neighbours():
+    """Rows whose gates take the plain form of silu, beside rows that take the one of any gate."""
+    _announce("matmul gates beside each other")
+    for T, N, K in ((24, 40, 64), (1040, 264, 64)):
+        m = list(make_matmul(T, 1, 1, N, K, "swiglu", False, "even", seed=T))
+        m[3] *= 8.0                                          # gates to some tens
+        plain = run_matmul(m, "swiglu", torch.float32)
+        m[1][::3] *= 1e3
+        mixed = run_matmul(m, "swiglu", torch.float32)
+        same = torch.arange(T) % 3 != 0
+        assert torch.equal(plain[same], mixed[same]) and torch.isfinite(plain).all()
 
 
 def test_expert_matmul_empty():
