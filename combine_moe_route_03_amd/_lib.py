@@ -413,13 +413,23 @@ def _opt(name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Optional
     return None if t is None else _arg(name, t, dtype, shape, device)
 
 
-def _matrix(name: str, t: torch.Tensor) -> torch.device:
-    """The device of a call, from its main input."""
+_MOST = 2 ** 31 - 1                   # the library's sizes are int32; ctypes would pass on low bits
+
+
+def _too_large(name: str, *sizes: int) -> None:
+    raise ValueError(f"{name}: size {max(sizes)}, needs at most {_MOST}")
+
+
+def _matrix(name: str, t: torch.Tensor):
+    """Device, rows and columns of a call, from its main input."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name}: a 2-d tensor is needed")
+    rows, cols = t.shape
+    if rows > _MOST or cols > _MOST:
+        _too_large(name, rows, cols)
     if not t.is_cuda:
         raise ValueError(f"{name}: on {t.device}, needs a GPU")
-    return t.device
+    return t.device, rows, cols
 
 
 def _empty(shape, dtype, device: torch.device, stream) -> torch.Tensor:
@@ -458,6 +468,8 @@ def _enqueue(fn: str, device: torch.device, stream, *args) -> None:
 
 @functools.lru_cache(maxsize=1024)
 def moe_balance_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
+    if max(T, E, n_seqs) > _MOST:
+        _too_large("T, E, n_seqs", T, E, n_seqs)
     return int(load().moe_balance_workspace_bytes(T, E, n_seqs))
 
 
@@ -476,10 +488,11 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     """Balance loss of the router; returns (loss [1], expert_counts [S,E], prob_sums [S,E],
     seq_tokens [S]). token_mask [T] bool or uint8: False marks padding. Without a workspace one
     is allocated for the call."""
-    dev = _matrix("logits", logits)
-    T, E = logits.shape
+    dev, T, E = _matrix("logits", logits)
     k = topk_idx.shape[-1]
     n_seqs = int(n_seqs)
+    if k > _MOST or n_seqs > _MOST:
+        _too_large("topk_idx" if k > _MOST else "n_seqs", k, n_seqs)
     if n_seqs < 1 or T % n_seqs:
         raise ValueError(f"n_seqs: {n_seqs} sequences do not divide {T} tokens")
     if loss is None:
@@ -516,10 +529,11 @@ def moe_route_grad(logits: torch.Tensor, topk_idx: torch.Tensor,
                    dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the router's logits [T,E]: of the balance loss (given expert_counts and
     seq_tokens), of the routing weights (given topk_w and dtopk_w), or their sum."""
-    dev = _matrix("logits", logits)
-    T, E = logits.shape
+    dev, T, E = _matrix("logits", logits)
     k = topk_idx.shape[-1]
     n_seqs = int(n_seqs)
+    if k > _MOST or n_seqs > _MOST:
+        _too_large("topk_idx" if k > _MOST else "n_seqs", k, n_seqs)
     if dlogits is None:
         dlogits = _empty((T, E), torch.float32, dev, stream)
     _enqueue("moe_route_grad", dev, stream,
@@ -540,8 +554,7 @@ def moe_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                    stream=None):
     """8-bit rows: (q int8 [R,H], scale fp32 [R]) with x about q * scale. n_rows (int32 [1] on
     the device): only the first n_rows rows are quantised."""
-    dev = _matrix("x", x)
-    R, H = x.shape
+    dev, R, H = _matrix("x", x)
     if q is None:
         q = _empty((R, H), torch.int8, dev, stream)
     if scale is None:
@@ -561,17 +574,20 @@ def moe_expert_matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor
     [E,N]; act "swiglu": [E,2N,K], gate channels first); returns out [R,N] in out's type or
     out_dtype. Row r of expert e (expert_offsets [E+1]) reads row row_token[r] of a, or row r
     without row_token. Without expert_offsets E must be 1: a plain product."""
-    dev = _matrix("a", a)
+    dev, A, K = _matrix("a", a)
     if act not in ACT_CODES:
         raise ValueError(f"act: {act!r}, needs one of {sorted(ACT_CODES)}")
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise TypeError("w: a 3-d tensor is needed")
-    A, K = a.shape
     E, n_w, _ = w.shape
+    if E > _MOST or n_w > _MOST:
+        _too_large("w", E, n_w)
     if act == "swiglu" and n_w % 2:
         raise ValueError(f"w: {n_w} channels do not split into gate and up")
     N = n_w // 2 if act == "swiglu" else n_w
     R = A if row_token is None else row_token.numel()
+    if R > _MOST:
+        _too_large("row_token", R)
     if out is None:
         out = _empty((R, N), out_dtype, dev, stream)
     _enqueue("moe_expert_matmul_i8", dev, stream, _arg("a", a, torch.int8, (A, K), dev),

@@ -781,3 +781,29 @@ def test_binding_refusals_on_the_gpu():
         moe.moe_expert_matmul_i8(a, sa, w, sw, off, act="relu")
     with pytest.raises(TypeError, match="out: dtype"):
         moe.moe_expert_matmul_i8(a, sa, w, sw, off, out_dtype=torch.float16)
+
+
+def test_binding_refuses_sizes_beyond_int32():
+    """Of every tensor that a size is taken from (tensors of one value, expanded: no memory)."""
+    _announce("binding sizes beyond int32")
+    def wide(dtype, *shape):
+        return torch.zeros(1, dtype=dtype, device="cuda").expand(shape)
+    over = 2 ** 32 + 16
+    x = torch.zeros((4, 16), device="cuda")
+    a, sa = torch.zeros((4, 16), dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    w, sw = torch.zeros((1, 8, 16), dtype=torch.int8, device="cuda"), torch.zeros((1, 8), device="cuda")
+    for name, call in (
+            ("logits", lambda: moe.moe_balance_loss(wide(torch.float32, over, 16), None, 0.1)),
+            ("topk_idx", lambda: moe.moe_balance_loss(x, wide(torch.int32, 4, over), 0.1)),
+            ("topk_idx", lambda: moe.moe_route_grad(x, wide(torch.int32, 4, over))),
+            ("n_seqs", lambda: moe.moe_balance_loss(x[:0], torch.zeros((0, 2), dtype=torch.int32,
+                                                                       device="cuda"), 0.1, over)),
+            ("n_seqs", lambda: moe.moe_route_grad(x, torch.zeros((4, 2), dtype=torch.int32,
+                                                                 device="cuda"), n_seqs=over)),
+            ("x", lambda: moe.moe_quant_rows(wide(torch.bfloat16, over, 16))),
+            ("w", lambda: moe.moe_expert_matmul_i8(a, sa, wide(torch.int8, 1, over, 16), sw)),
+            ("w", lambda: moe.moe_expert_matmul_i8(a, sa, wide(torch.int8, over, 8, 16), sw)),
+            ("row_token", lambda: moe.moe_expert_matmul_i8(a, sa, w, sw,
+                                                           row_token=wide(torch.int32, over)))):
+        with pytest.raises(ValueError, match=f"{name}: .*2147483647"):
+            call()

@@ -134,6 +134,23 @@ def test_binding_refuses_tensors_that_do_not_fit():
         moe.moe_quant_rows(torch.zeros(3))
 
 
+def test_binding_refuses_sizes_beyond_int32():
+    """The library takes int32 sizes, and ctypes would pass on their low 32 bits: 2^32 + 64 rows would
+    be 64."""
+    over = 2 ** 32 + 64
+    idx = torch.empty((over, 1), dtype=torch.int32, device="meta")
+    for shape in ((over, 16), (16, over)):
+        x = torch.empty(shape, device="meta")
+        for call in (lambda: moe.moe_balance_loss(x, idx, 0.01), lambda: moe.moe_route_grad(x, idx),
+                     lambda: moe.moe_quant_rows(x), lambda: moe.moe_expert_matmul_i8(x, x, x, x)):
+            with pytest.raises(ValueError, match="2147483647"):
+                call()
+    for sizes in ((over, 1, 1), (64, over, 1), (0, 1, over)):
+        with pytest.raises(ValueError, match="2147483647"):
+            moe.moe_balance_workspace_bytes(*sizes)
+    assert moe.moe_balance_workspace_bytes(64, 16, 4) > 0
+
+
 def test_plain_gradient_against_differences():
     """The gradient's formula against central differences of the loss and of the routing weights in
     64 bits: off by at most h^2 max |c| f (third derivatives of p) and by cancellation."""
