@@ -580,7 +580,7 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
 __device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
+                 :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "m0", "memory");
 }
 
 // All but the PENDING youngest of this wavefront's loads are in LDS.
