@@ -576,11 +576,12 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
 
 // 16 bytes a lane from `buffer` at voff + soff to LDS at lds + 16 * lane. In asm, since the
 // compiler would wait for all such loads before every LDS read; it has no register output, and
-// wait_loads() waits for it.
+// wait_loads() waits for it. The compiler puts the LDS address into m0 itself, so that it knows what
+// is in there; s_nop is the wait state between that and the load.
 __device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t voff, uint32_t soff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "m0", "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "{m0}"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
 }
 
 // All but the PENDING youngest of this wavefront's loads are in LDS.
