@@ -5,8 +5,10 @@
 //   loss = alpha / S * E / (k n^2) * sum_e c_e P_e,   d loss / d l_te = f p_te (c_e - sum_i c_i p_ti)
 // with f = alpha / S * E / (k n^2), since d p_i / d l_e = p_i (delta_ie - p_e). The forward pass
 // reads the logits once, the backward pass reads them again (4 bytes an element, against writing
-// and reading the probabilities) and writes the gradient once: both are bound by HBM, and by the
-// latency of their launches for small batches.
+// and reading the probabilities) and writes the gradient once. Small batches are bound by their
+// launches, long ones by the vector instructions next to HBM: of 256 experts a token takes 93 in the
+// forward pass and 245 in the backward one with the weights' part, which keeps the SIMDs busy for 11
+// of its 16 us and for 28 of its 31 us (65536 tokens, k = 8).
 #include "moe_device.h"
 #include "moe_layer.h"
 
@@ -19,7 +21,12 @@ constexpr int kLossWaves = kLossThreads / 64;
 constexpr int kGradThreads = 256;
 constexpr int kMaxLossBlocks = 512;      // workgroups of the forward pass, two a CU
 constexpr int kLossTokens = 32;          //   of no fewer tokens than two a wavefront
-constexpr int kDirectTokens = 192;       // one workgroup and one launch up to so many tokens
+// One workgroup and one launch up to so many tokens: a token costs its 93 instructions on one CU
+// (256 experts: 0.038 us), a second launch about 4 us of the GPU and 3 of the host. us by one launch
+// and by two, launches alone: 64 tokens 4.2 and 8.0 (64 experts), 5.8 and 8.7 (256), 9.2 and 11.0
+// (1024); 192 tokens 5.2 and 8.2, 11.1 and 9.1, 19.8 and 11.1. (With more than 64 experts the limit by
+// these figures would be lower, with fewer higher.)
+constexpr int kDirectTokens = 192;
 constexpr int kFinishExperts = 32;       // experts of a finishing workgroup
 constexpr int kFinishThreads = 512;      //   by 16 slices of the partial sums
 constexpr int kFinishSlices = kFinishThreads / kFinishExperts;

@@ -3,8 +3,9 @@
 //   k_quant_rows   q = rint(127 x / max |x|), scale = max |x| / 127: one pass, bound by HBM.
 //   k_matmul_tile  y_rn = (sum_i a_ri w_eni) a_scale_r w_scale_en, and SwiGLU of two channels: tiles
 //                  of 32 to 256 rows of one expert. With few rows an expert the weights' bytes bound
-//                  it (128 tokens over 256 experts: 7.5 GB in 1.19 ms, 6.3 TB/s), with many the
-//                  matrix cores and the LDS that feeds them (8192^3: 2.3 to 2.4 POPS).
+//                  it (128 tokens over 256 experts: 7.4 GB in 1.19 ms, 6.2 TB/s), with many the
+//                  matrix cores and the LDS that feeds them (8192^3: 456 to 500 us on different
+//                  boxes, 2.2 to 2.4 POPS).
 //   k_matmul_few   the same where there are too few tiles to fill the GPU: the wavefronts of a
 //                  workgroup share K (one row by 29 MB of weights: 7.7 us).
 #include <atomic>
@@ -269,7 +270,7 @@ void launch_quant_g(const void* x, int32_t R, int32_t H, const int32_t* n_rows, 
 // Lanes of a row: few enough that each has two to four vectors in flight, so many that a row's
 // registers leave room for other rows. 32768 rows in bf16: 1408 elements 30 us with 64 lanes, 33
 // with 128, 37 with 256; 2048: 40, 39, 44; 4096: 81, 73, 73 (5.5 TB/s), 91 with 512; 4096 rows of
-// 7168: 20, 20, 18, 18.
+// 7168: 20, 20, 18, 18. In fp32, as chosen here, 32768 rows of 4096 take 125 us (5.4 TB/s).
 template <typename V>
 void launch_quant(const void* x, int32_t R, int32_t H, const int32_t* n_rows, int8_t* q,
                   float* scale, hipStream_t stream)
@@ -555,12 +556,18 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
 // lane l the 16-byte piece (l % 8) ^ (l / 8) of line l / 8, so that piece c of line r lies in slot
 // c ^ (r % 8) and the operand reads (the same piece of consecutive lines) fall on different banks.
 // Operands of a quarter step are read while the quarter before is multiplied, and the loads go on
-// into the next tile while a tile's results are written.
+// into the next tile: its first stages are asked for before a tile's results are written.
 //   A step of a 256 x 256 tile is 2048 cycles of MFMA (v_mfma_i32_32x32x32_i8, 8 wavefronts of 128 x
-// 64), and 2048 of LDS at 128 bytes a cycle: 64 KiB in, 192 KiB out. With no loads and no reads the
-// loop of 8192^3 takes 320 us, with loads 375, with reads and loads 450. Steps of 64 bytes (half
+// 64), and 2048 of LDS at 128 bytes a cycle: 64 KiB in, 192 KiB out. Of 8192^3, 496 us, 410 are left
+// without the LDS reads, 316 without the products, 303 with the loads alone. Steps of 64 bytes (half
 // lines a load, twice the barriers) take 562 us against 509, four wavefronts of 128 x 128 (less LDS,
 // one wavefront a SIMD) 510 against 488, loads spread among the products 484 against 477.
+//   A tile's beginning waits: its rows' tokens and its channels' scales come by ordinary loads, and
+// the compiler waits for the first of them before the first product, in every instance. vmcnt counts
+// in order, so the last tile's stores and the stages read ahead are waited for with it; aim(), which
+// reads offsets and row tokens, waits as well. Where a tile has few steps this shows (16 steps, 384
+// experts: 1.12 ms for 0.95 of bytes). The 256 x 256 instances also keep 6 to 11 registers in scratch,
+// which they read at a tile's beginning and end, not among the products.
 constexpr int kStepK = 128;
 
 __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
@@ -855,7 +862,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
     const auto landed = [&](int32_t next, bool partial) {
         if (ahead < STAGES - 1)
             wait_loads<0>();
-        else if (older > 0)                                   // the stores may still be on their way
+        else if (older > 0)                                   // without the stores behind it
             wait_loads<(STAGES - 2) * kLoads + kStores>();
         else
             wait_loads<(STAGES - 2) * kLoads>();
@@ -931,7 +938,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
             landed(next, ragged && step == steps - 2);
             wait_workgroup();                                 // and this stage is read
             --ahead;
-            if (step == 1)                                    // a wait for the row, which is there
+            if (step == 1)                                    // (the row came at the beginning)
                 scale();
             issue();
             at = next;
@@ -965,8 +972,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
         // Results, while the next tile's first stages are on their way: the lane's fp32 values are
         // rounded, go through a little LDS of the wavefront's own, and come back as rows of 128
         // bytes (bf16) for 16-byte stores; 16-byte piece c of row r lies in slot c ^ (r % 8).
-        // Stores of whole rows count the same for every wavefront, so that the loads before them
-        // can be waited for without them. (Stored from the accumulators two bytes at a time, the
+        // Stores of whole rows count the same for every wavefront, so that landed() can wait for the
+        // loads before them without them; the next tile's ordinary loads still wait for them, see
+        // above. (Stored from the accumulators two bytes at a time, the
         // results of 8192^3 took 150 of 621 us; with the stores waited for at once, 50 of 470.)
         constexpr int kPieces = kUnitRow / 16;
         const bool wide = p.N % (16 / (int)sizeof(OUT)) == 0 && (uintptr_t)p.out % 16 == 0 &&
