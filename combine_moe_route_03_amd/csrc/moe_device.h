@@ -1,4 +1,4 @@
-// moe_device.h -- device and host helpers shared by moe_balance.hip and moe_experts.hip.
+// moe_device.h -- device and host helpers shared by the operators next to routing.
 #ifndef MOE_DEVICE_H
 #define MOE_DEVICE_H
 

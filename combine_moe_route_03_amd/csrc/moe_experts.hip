@@ -10,8 +10,8 @@
 //                  workgroup share K (one row by 29 MB of weights: 7.7 us).
 #include <atomic>
 
-#include "moe_device.h"
 #include "moe_layer.h"
+#include "moe_tiles.h"
 
 namespace {
 
@@ -23,8 +23,6 @@ using namespace moe_dev;
 // for an element. G lanes take a row, with up to NV vectors of 8 elements a lane in flight at once.
 // Rows beyond 512 lanes of 8 vectors are read a second time, from the cache.
 constexpr int kQuantVec = 8;
-constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
-constexpr int kCus = 256;
 
 // Eight elements as they are in memory.
 struct Bf16x8 {
@@ -304,119 +302,6 @@ struct MatmulArgs {
     double inv_blocks;         // 1 / n_blocks
 };
 
-// Rows [row0, row0 + rows) of expert e, channel block n; rows = 0: nothing to do.
-struct Tile {
-    int32_t e, row0, rows, n;
-};
-
-// Rows of expert e and the first of them. Offsets are clamped into [0, R], so no value of theirs
-// leads outside the rows.
-__device__ __forceinline__ int32_t expert_rows(const MatmulArgs& p, int32_t e, int32_t* lo)
-{
-    if (!p.offsets) {
-        *lo = 0;
-        return p.R;
-    }
-    *lo = min(max(p.offsets[e], 0), p.R);
-    return min(max(p.offsets[e + 1], *lo), p.R) - *lo;
-}
-
-// Row tile `index` of all experts' tiles of BM rows, found by each wavefront for itself: a lane
-// adds up the tiles of its share of the experts, a scan over the lanes finds the share that holds
-// the index.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int32_t index)
-{
-    const int lane = threadIdx.x & 63;
-    int32_t mine = 0, lo = 0;
-    if (p.E == 1) {
-        const int32_t rows = expert_rows(p, 0, &lo);
-        return Tile{0, lo + index * BM, max(0, min(BM, rows - index * BM)), 0};
-    }
-    const int per = (p.E + 63) / 64;
-    const int e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
-    for (int e = e0; e < e1; ++e)
-        mine += (expert_rows(p, e, &lo) + BM - 1) / BM;
-    int32_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int32_t o = __shfl_up(upto, d);
-        if (lane >= d)
-            upto += o;
-    }
-    const int32_t before = upto - mine;
-    const uint64_t holds = __ballot(before <= index && index < upto);
-    if (holds == 0)
-        return Tile{0, 0, 0, 0};
-    const int at = __ffsll((unsigned long long)holds) - 1;
-    int32_t e = __builtin_amdgcn_readlane(e0, at);
-    int32_t left = index - __builtin_amdgcn_readlane(before, at), n;
-    for (;; ++e) {
-        n = expert_rows(p, e, &lo);
-        const int32_t tiles = (n + BM - 1) / BM;
-        if (left < tiles)
-            break;
-        left -= tiles;
-    }
-    return Tile{e, __builtin_amdgcn_readfirstlane(lo + left * BM),
-                __builtin_amdgcn_readfirstlane(min(BM, n - left * BM)), 0};
-}
-
-// gate / (1 + exp(-gate)), with exp(x) = 2^(x log2 e): the product's rounding, |gate| 2^-24 of the
-// result, is added back to first order; v_exp_f32 and v_rcp_f32 are good to one ulp. FAR: any gate.
-// Above t = 96, where 1 is nothing next to exp, both work on its root and silu is
-// gate / sqrt(exp) / sqrt(exp): exp itself overflows from t = 128 (gate -88.7) and its reciprocal is
-// flushed from 126, but silu is a normal number down to gate -92. Beyond |t| = 192 the root goes
-// without its correction, which an infinite t would make infinite or NaN.
-template <bool FAR>
-__device__ __forceinline__ float silu(float gate)
-{
-    constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
-    const float t = gate * hi;
-    const float rest = (__builtin_fmaf(gate, hi, -t) + gate * lo) * 0.693147182f;
-    if (!FAR) {
-        const float e = __builtin_amdgcn_exp2f(t);
-        return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest, e));
-    }
-    const bool far = t > 96.0f;
-    const float half = far ? 0.5f : 1.0f;
-    const float e = __builtin_amdgcn_exp2f(t * half);
-    const float s = __builtin_fabsf(t) > 192.0f ? e : __builtin_fmaf(e, rest * half, e);
-    const float r = __builtin_amdgcn_rcpf((far ? 0.0f : 1.0f) + s);
-    return gate * r * (far ? r : 1.0f);
-}
-
-// silu(gate) * up of four channels. Gates up to 64 have the same bits by both forms, so a row's
-// results do not depend on what else is in its wavefront. (The form for any gate alone: 16384 rows
-// over 4 experts, 4096 channels of K = 512, 140 us against 130; 2048 tokens over 64 experts of 2048
-// by 4096 390 against 377.)
-__device__ __forceinline__ f32x4 swiglu(f32x4 gate, f32x4 up)
-{
-    const float most = fmaxf(fmaxf(__builtin_fabsf(gate[0]), __builtin_fabsf(gate[1])),
-                             fmaxf(__builtin_fabsf(gate[2]), __builtin_fabsf(gate[3])));
-    f32x4 y;
-    if (__builtin_expect(!__any(most > 64.0f), 1)) {          // a NaN may go either way
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            y[c] = silu<false>(gate[c]) * up[c];
-    } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            y[c] = silu<true>(gate[c]) * up[c];
-    }
-    return y;
-}
-
-// Four results as they are kept in memory.
-template <typename OUT>
-struct Four {
-    typedef f32x4 type;
-};
-template <>
-struct Four<__bf16> {
-    typedef bf16x4 type;
-};
-
 // Few rows an expert: bound by reading the weights, each once. A workgroup takes up to 16 MF rows
 // of one expert and 16 NF channels; its wavefronts share the K axis out by 128-byte pieces, read
 // weights and rows straight into MFMA operands, and add their int32 sums up through LDS (integers:
@@ -569,133 +454,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_matmul_few(MatmulArgs p)
 // experts: 1.12 ms for 0.95 of bytes). The 256 x 256 instances also keep 6 to 11 registers in scratch,
 // which they read at a tile's beginning and end, not among the products.
 constexpr int kStepK = 128;
-
-__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes)
-{
-    const uint64_t b = (uint64_t)(uintptr_t)base;
-    u32x4 r;
-    r[0] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
-    r[1] = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu));
-    r[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
-    r[3] = 0x00020000u;
-    return r;
-}
-
-// 16 bytes a lane from `buffer` at voff + soff to LDS at lds + 16 * lane. In asm, since the
-// compiler would wait for all such loads before every LDS read; it has no register output, and
-// wait_loads() waits for it. The compiler puts the LDS address into m0 itself, so that it knows what
-// is in there; s_nop is the wait state between that and the load.
-__device__ __forceinline__ void load_lds(u32x4 buffer, uint32_t voff, uint32_t soff, uint32_t lds)
-{
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "{m0}"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
-}
-
-// All but the PENDING youngest of this wavefront's loads are in LDS.
-template <int PENDING>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(PENDING) : "memory");
-}
-
-// This wavefront's LDS accesses are done, and so are those of the others of the workgroup.
-__device__ __forceinline__ void wait_workgroup()
-{
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// 16 bytes to `buffer` at voff, dropped where that is out of its range. Not for the caches: the
-// next kernel reads the results from their start, and only the last ones would still be there.
-__device__ __forceinline__ void store_buffer(u32x4 v, __amdgpu_buffer_rsrc_t buffer, uint32_t voff)
-{
-    __builtin_amdgcn_raw_buffer_store_b128(v, buffer, voff, 0, 2 /* nt */);
-}
-
-// Exclusive prefix of the experts' row tiles into prefix[0 .. E] (every thread calls), and their
-// total; 0 if that is more than rising offsets can give.
-template <int THREADS, int BM>
-__device__ __forceinline__ int32_t tile_prefix(const MatmulArgs& p, int32_t* prefix)
-{
-    __shared__ int64_t s_wave[THREADS / 64];
-    const int tid = threadIdx.x;
-    const int per = (p.E + THREADS - 1) / THREADS;
-    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
-    const auto tiles = [&](int32_t e) {
-        int32_t lo;
-        const int32_t n = expert_rows(p, e, &lo);
-        return n / BM + (n % BM != 0);
-    };
-    int64_t mine = 0;
-    for (int e = e0; e < e1; ++e)
-        mine += tiles(e);
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up((long long)upto, d);
-        if ((tid & 63) >= d)
-            upto += o;
-    }
-    if ((tid & 63) == 63)
-        s_wave[tid >> 6] = upto;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-        if (w < (tid >> 6))
-            upto += s_wave[w];
-        total += s_wave[w];
-    }
-    if (total > p.max_tiles)
-        return 0;
-    int32_t at = (int32_t)(upto - mine);
-    for (int e = e0; e < e1; ++e) {
-        prefix[e] = at;
-        at += tiles(e);
-    }
-    if (tid == 0)
-        prefix[p.E] = (int32_t)total;
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane((int32_t)total);
-}
-
-// x / n of the same value in every lane, x >= 0, by inv = 1 / n in fp64: off by one at most.
-__device__ __forceinline__ int32_t quotient(int32_t x, int32_t n, double inv)
-{
-    int32_t q = __builtin_amdgcn_readfirstlane((int32_t)((double)x * inv));
-    const int32_t r = x - q * n;
-    q -= r < 0;
-    q += r >= n;
-    return q;
-}
-
-// Tile `at` of all: expert by expert, GROUP row tiles by all channel blocks at a time, row tiles
-// fastest, so that tiles that run together on an XCD share weights and rows in its L2.
-template <int BM, int GROUP>
-__device__ __forceinline__ Tile tile_at(const MatmulArgs& p, const int32_t* prefix, int32_t at)
-{
-    static_assert(GROUP == 4, "side is at most 4");
-    const int32_t index = quotient(at, p.n_blocks, p.inv_blocks);
-    int32_t e = -1;
-    for (int j = 0; j < p.E; j += 64) {
-        const int i = j + (threadIdx.x & 63);
-        e += __popcll(__ballot(i < p.E && prefix[i] <= index));
-    }
-    const int32_t before = __builtin_amdgcn_readfirstlane(prefix[e]);
-    const int32_t tiles = __builtin_amdgcn_readfirstlane(prefix[e + 1]) - before;
-    const int32_t local = at - before * p.n_blocks;
-    const int32_t group = quotient(local, GROUP * p.n_blocks, p.inv_blocks / GROUP);
-    const int32_t in = local - group * GROUP * p.n_blocks;
-    const int32_t side = min(GROUP, tiles - group * GROUP);
-    Tile t;
-    t.e = e;
-    t.n = side == 4 ? in >> 2 : side == 3 ? (int32_t)((uint32_t)in / 3u) : side == 2 ? in >> 1 : in;
-    const int32_t m = group * GROUP + in - t.n * side;
-    int32_t lo;
-    const int32_t n = expert_rows(p, e, &lo);
-    t.row0 = __builtin_amdgcn_readfirstlane(lo + m * BM);
-    t.rows = __builtin_amdgcn_readfirstlane(min(BM, n - m * BM));
-    return t;
-}
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
@@ -1064,18 +822,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(MatmulArgs p)
             }
         }
     }
-}
-
-// Workgroups for tiles of bm rows: the row tiles of all experts are at most R / bm and one more for
-// each expert that has rows.
-inline int64_t most_tiles(const MatmulArgs& p, int32_t bm)
-{
-    return p.offsets ? p.R / bm + (p.E < p.R ? p.E : p.R) : div_up(p.R, bm);
-}
-
-inline moe_status_t launched()
-{
-    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
