@@ -1,7 +1,8 @@
 """MI355X (gfx950) MoE token routing: top-k routing, dispatch into per-rank receive buffers, and
 weighted combine, as hand-written HIP kernels behind the C ABI of include/moe_route.h; and the
-operators next to it, of include/moe_layer.h: the router's balance loss and gradient, 8-bit rows,
-and the experts' product in 8-bit integers.
+operators next to it: of include/moe_layer.h, the router's balance loss and gradient, 8-bit rows, and
+the experts' product in 8-bit integers; of include/moe_block.h, scored routing with a bias and groups,
+the experts' product in bf16, and their gradients.
 
 The binding functions carry the C names; importing them loads libmoe_route.so and fails loudly if
 it has not been built.
@@ -14,7 +15,9 @@ _EXPORTS = ("moe_route_topk", "moe_dispatch_workspace_bytes", "moe_dispatch_layo
             "moe_ep_combine", "moe_ep_partial_rows", "moe_ep_reduce", "moe_ep_reduce_workspace",
             "moe_ep_combine_reduced", "moe_check_topk", "moe_balance_workspace_bytes",
             "alloc_balance_workspace", "moe_balance_loss", "moe_route_grad", "moe_quant_rows",
-            "moe_expert_matmul_i8")
+            "moe_expert_matmul_i8", "moe_route_scored", "moe_route_scored_grad", "moe_bias_update",
+            "moe_combine_grad", "moe_expert_matmul", "moe_expert_matmul_grad",
+            "moe_matmul_grad_workspace_bytes", "alloc_matmul_grad_workspace")
 
 
 def __getattr__(name):

@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe_route.so (include/moe_route.h, include/moe_layer.h), with the C names.
+"""ctypes binding of libmoe_route.so (include/moe_route.h, include/moe_layer.h, include/moe_block.h),
+with the C names.
 
 Argument marshalling only: torch tensors supply device memory and the current HIP stream, and
 every step runs in the library's HIP kernels. If the library is not built, loading fails with an
@@ -26,6 +27,13 @@ MOE_MAX_SEQS = 65536
 MOE_MATMUL_MAX_K = 131056
 MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 ACT_CODES = {"none": MOE_ACT_NONE, "swiglu": MOE_ACT_SWIGLU}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORE_CODES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_MAX_GROUPS = 64
+MOE_MAT_NONE, MOE_MAT_SWIGLU, MOE_MAT_RELU, MOE_MAT_SILU, MOE_MAT_GELU = range(5)
+MAT_ACT_CODES = {"none": MOE_MAT_NONE, "swiglu": MOE_MAT_SWIGLU, "relu": MOE_MAT_RELU,
+                 "silu": MOE_MAT_SILU, "gelu": MOE_MAT_GELU}
+MOE_MAT_MAX_SIZE = 4194304
 
 DTYPE_CODES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3}
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8_e4m3": torch.uint8}
@@ -83,10 +91,20 @@ def load() -> ctypes.CDLL:
         lib.moe_route_grad.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, F, P, P]
         lib.moe_quant_rows.argtypes = [P, I, I, I, P, P, P, P]
         lib.moe_expert_matmul_i8.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, P, I, P]
-        for fn in ("moe_balance_loss", "moe_route_grad", "moe_quant_rows", "moe_expert_matmul_i8",
+        lib.moe_route_scored.argtypes = [P, P, I, I, I, I, I, I, I, I, F, P, P, P]
+        lib.moe_route_scored_grad.argtypes = [P, P, P, P, I, I, I, I, I, F, P, P]
+        lib.moe_bias_update.argtypes = [P, P, I, I, F, P, P]
+        lib.moe_combine_grad.argtypes = [P, I, P, I, P, P, I, I, I, P, P, P]
+        lib.moe_expert_matmul.argtypes = [P, I, P, P, P, P, I, I, I, I, I, P, P, P, I, P]
+        lib.moe_matmul_grad_workspace_bytes.argtypes = [I, I, I, I]
+        lib.moe_matmul_grad_workspace_bytes.restype = Z
+        lib.moe_expert_matmul_grad.argtypes = [P, P, I, P, P, P, I, I, I, I, I, P, P, I, P, I, P, P, Z,
+                                               P]
+        for fn in ("moe_route_scored", "moe_route_scored_grad", "moe_bias_update", "moe_combine_grad",
+                   "moe_expert_matmul", "moe_expert_matmul_grad", "moe_balance_loss", "moe_route_grad", "moe_quant_rows", "moe_expert_matmul_i8",
                    "moe_route_topk", "moe_dispatch_layout", "moe_dispatch_pack", "moe_dispatch",
-                   "moe_route_dispatch", "moe_route_dispatch_noalloc", "moe_combine", "moe_ep_send", "moe_ep_recv",
-                   "moe_ep_return", "moe_ep_combine", "moe_ep_partial_rows", "moe_ep_reduce",
+                   "moe_route_dispatch", "moe_route_dispatch_noalloc", "moe_combine", "moe_ep_send",
+                   "moe_ep_recv", "moe_ep_return", "moe_ep_combine", "moe_ep_partial_rows", "moe_ep_reduce",
                    "moe_ep_combine_reduced", "moe_check_topk"):
             getattr(lib, fn).restype = I
         _lib = lib
@@ -598,3 +616,219 @@ def moe_expert_matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor
              _opt("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev), R, E, N, K,
              ACT_CODES[act], _arg("out", out, _WIDE, (R, N), dev), _dtype_code(out))
     return out
+
+
+# ------------------------------------------------------------------------------------------------
+# Scored routing, the experts' product in bf16, and their gradients (see include/moe_block.h), with
+# the same checks.
+
+def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax",
+                     bias: Optional[torch.Tensor] = None, n_groups: int = 1, topk_groups: int = 1,
+                     group_top: int = 2, renormalize: bool = True, scale: float = 1.0,
+                     topk_idx: Optional[torch.Tensor] = None,
+                     topk_w: Optional[torch.Tensor] = None, stream=None):
+    """Scored routing of logits [T,E]: (expert ids int32 [T,k], weights fp32 [T,k]). Scores are
+    "softmax" or "sigmoid"; bias [E] takes part in the choice only; with n_groups > 1 the experts of
+    the topk_groups groups with the largest sums of their group_top best are chosen from. Weights are
+    the chosen scores, over their sum if renormalize, times scale."""
+    dev, T, E = _matrix("logits", logits)
+    if score not in SCORE_CODES:
+        raise ValueError(f"score: {score!r}, needs one of {sorted(SCORE_CODES)}")
+    k, n_groups, topk_groups, group_top = int(k), int(n_groups), int(topk_groups), int(group_top)
+    if max(k, n_groups, topk_groups, group_top) > _MOST or min(k, n_groups, topk_groups, group_top) < 0:
+        raise ValueError(f"k, n_groups, topk_groups, group_top: {k}, {n_groups}, {topk_groups}, "
+                         f"{group_top}")
+    if topk_idx is None:
+        topk_idx = _empty((T, k), torch.int32, dev, stream)
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, dev, stream)
+    _enqueue("moe_route_scored", dev, stream, _arg("logits", logits, torch.float32, (T, E), dev),
+             _opt("bias", bias, torch.float32, (E,), dev), T, E, k, SCORE_CODES[score], n_groups,
+             topk_groups, group_top, int(bool(renormalize)), float(scale),
+             _arg("topk_idx", topk_idx, torch.int32, (T, k), dev),
+             _arg("topk_w", topk_w, torch.float32, (T, k), dev))
+    return topk_idx, topk_w
+
+
+def moe_route_scored_grad(logits: torch.Tensor, topk_idx: torch.Tensor, dtopk_w: torch.Tensor,
+                          score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                          add: Optional[torch.Tensor] = None,
+                          dlogits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits [T,E] through the weights of moe_route_scored, plus add [T,E] (which may
+    be dlogits itself)."""
+    dev, T, E = _matrix("logits", logits)
+    if score not in SCORE_CODES:
+        raise ValueError(f"score: {score!r}, needs one of {sorted(SCORE_CODES)}")
+    k = topk_idx.shape[-1]
+    if k > _MOST:
+        _too_large("topk_idx", k)
+    if dlogits is None:
+        dlogits = _empty((T, E), torch.float32, dev, stream)
+    _enqueue("moe_route_scored_grad", dev, stream,
+             _arg("logits", logits, torch.float32, (T, E), dev),
+             _arg("topk_idx", topk_idx, torch.int32, (T, k), dev),
+             _arg("dtopk_w", dtopk_w, torch.float32, (T, k), dev),
+             _opt("add", add, torch.float32, (T, E), dev), T, E, k, SCORE_CODES[score],
+             int(bool(renormalize)), float(scale),
+             _arg("dlogits", dlogits, torch.float32, (T, E), dev))
+    return dlogits
+
+
+def moe_bias_update(bias: torch.Tensor, expert_counts: torch.Tensor, rate: float,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Balance biases [L,E] (or [E]) after a step: plus rate where an expert's count is below its
+    layer's mean, minus rate where it is above. out may be bias itself."""
+    if not isinstance(bias, torch.Tensor) or bias.dim() not in (1, 2):
+        raise TypeError("bias: a 1-d or 2-d tensor is needed")
+    dev, L, E = _matrix("bias", bias if bias.dim() == 2 else bias[None])
+    if out is None:
+        out = _empty(bias.shape, torch.float32, dev, stream)
+    _enqueue("moe_bias_update", dev, stream, _arg("bias", bias, torch.float32, bias.shape, dev),
+             _arg("expert_counts", expert_counts, torch.int32, bias.shape, dev), L, E, float(rate),
+             _arg("out", out, torch.float32, bias.shape, dev))
+    return out
+
+
+def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], token_row: torch.Tensor,
+                     topk_w: torch.Tensor, dy: Optional[torch.Tensor] = None,
+                     dtopk_w: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine from dout [T,H]: (dy [T*k,H], dtopk_w [T,k]). Without y only dy is
+    computed (in dy's type, bf16 if it is not given) and dtopk_w is None."""
+    dev, T, H = _matrix("dout", dout)
+    k = topk_w.shape[-1]
+    if k > _MOST or T * k > _MOST:
+        _too_large("topk_w", k, T * k)
+    wide = y if y is not None else dy
+    y_dtype = torch.bfloat16 if wide is None else wide.dtype
+    if dy is None:
+        dy = _empty((T * k, H), y_dtype, dev, stream)
+    if y is not None and dtopk_w is None:
+        dtopk_w = _empty((T, k), torch.float32, dev, stream)
+    if y is None and dtopk_w is not None:
+        raise ValueError("dtopk_w: needs y")
+    _enqueue("moe_combine_grad", dev, stream, _arg("dout", dout, _WIDE, (T, H), dev),
+             _dtype_code(dout), _opt("y", y, _WIDE, (T * k, H), dev), _dtype_code(dy),
+             _arg("token_row", token_row, torch.int32, (T * k,), dev),
+             _arg("topk_w", topk_w, torch.float32, (T, k), dev), T, H, k,
+             _arg("dy", dy, y_dtype, (T * k, H), dev),
+             _opt("dtopk_w", dtopk_w, torch.float32, (T, k), dev))
+    return dy, dtopk_w
+
+
+def _product_sizes(w: torch.Tensor, act: str, R: int):
+    if act not in MAT_ACT_CODES:
+        raise ValueError(f"act: {act!r}, needs one of {sorted(MAT_ACT_CODES)}")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w: a 3-d tensor is needed")
+    if R > _MOST:
+        _too_large("row_token", R)
+    E, n_w, K = w.shape
+    if max(E, n_w, K) > _MOST:
+        _too_large("w", E, n_w, K)
+    return E, n_w, K
+
+
+def moe_expert_matmul(a: torch.Tensor, w: torch.Tensor,
+                      expert_offsets: Optional[torch.Tensor] = None,
+                      row_token: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, act: str = "none",
+                      residual: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The experts' product of bf16 rows a [A,K] with bf16 weights w [E,N,K] (act "swiglu": [E,2N,K],
+    gate channels first): act(a w^T + bias) + residual, out [R,N] in out's type or out_dtype. act is
+    "none", "relu", "silu", "gelu" (tanh form) or "swiglu"; bias [E,N or 2N] fp32; residual [R,N] in
+    out's type, it may be out; pre [R,N or 2N] bf16 gets the sums before the activation. Row r of expert
+    e (expert_offsets [E+1]) reads row row_token[r] of a, or row r without row_token. Without
+    expert_offsets E must be 1: a plain product."""
+    dev, A, K = _matrix("a", a)
+    R = A if row_token is None else row_token.numel()
+    E, n_w, _ = _product_sizes(w, act, R)
+    if act == "swiglu" and n_w % 2:
+        raise ValueError(f"w: {n_w} channels do not split into gate and up")
+    N = n_w // 2 if act == "swiglu" else n_w
+    if out is None:
+        out = _empty((R, N), out_dtype, dev, stream)
+    _enqueue("moe_expert_matmul", dev, stream, _arg("a", a, torch.bfloat16, (A, K), dev), A,
+             _opt("row_token", row_token, torch.int32, (R,), dev),
+             _arg("w", w, torch.bfloat16, (E, n_w, K), dev),
+             _opt("bias", bias, torch.float32, (E, n_w), dev),
+             _opt("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev), R, E, N, K,
+             MAT_ACT_CODES[act], _opt("residual", residual, out.dtype, (R, N), dev),
+             _opt("pre", pre, torch.bfloat16, (R, n_w), dev),
+             _arg("out", out, _WIDE, (R, N), dev), _dtype_code(out))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_matmul_grad_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    if max(R, E, N, K) > _MOST:
+        _too_large("R, E, N, K", R, E, N, K)
+    return int(load().moe_matmul_grad_workspace_bytes(R, E, N, K))
+
+
+def alloc_matmul_grad_workspace(R: int, E: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    n = max(moe_matmul_grad_workspace_bytes(R, E, N, K), 1)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_expert_matmul_grad(dy: torch.Tensor, a: Optional[torch.Tensor], w: torch.Tensor,
+                           expert_offsets: Optional[torch.Tensor] = None, want=("da", "dw"),
+                           row_token: Optional[torch.Tensor] = None, act: str = "none",
+                           pre: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
+                           dw: Optional[torch.Tensor] = None,
+                           dbias: Optional[torch.Tensor] = None,
+                           da_dtype: torch.dtype = torch.bfloat16,
+                           dw_dtype: torch.dtype = torch.float32,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of the product a w^T + bias from dy [R,N] bf16: a tuple of those that `want` names, in
+    its order. "da" [R,K], one row for each row of dy (with row_token, moe_combine with weights of one
+    adds up a token's); "dw" [E,N,K]; "dbias" [E,N] fp32. With an activation, a was act(pre) and da is
+    the gradient of pre ([R,K]; "swiglu": pre and da [R,2K]). a may be None if only "da" is wanted and
+    row_token is not given. Without a workspace one is allocated for the call."""
+    dev, R, N = _matrix("dy", dy)
+    E, _, K = _product_sizes(w, act, R)
+    want = (want,) if isinstance(want, str) else tuple(want)
+    if not want or len(set(want)) != len(want) or not set(want) <= {"da", "dw", "dbias"}:
+        raise ValueError(f"want: {want!r}, needs some of 'da', 'dw', 'dbias', each once")
+    if a is None and ("dw" in want or row_token is not None):
+        raise ValueError("a: needed for 'dw', and with row_token")
+    A = R if a is None else _matrix("a", a)[1]
+    if "da" in want:
+        n_a = 2 * K if act == "swiglu" else K
+        if act != "none" and pre is None:
+            raise ValueError(f"pre: needed for act {act!r}")
+        if da is None:
+            da = _empty((R, n_a), da_dtype, dev, stream)
+        _arg("da", da, _WIDE, (R, n_a), dev)
+        _opt("pre", pre, torch.bfloat16, (R, n_a), dev)
+    else:
+        da = None
+    if "dw" in want:
+        if dw is None:
+            dw = _empty((E, N, K), dw_dtype, dev, stream)
+        _arg("dw", dw, _WIDE, (E, N, K), dev)
+    else:
+        dw = None
+    if "dbias" in want:
+        if dbias is None:
+            dbias = _empty((E, N), torch.float32, dev, stream)
+        _arg("dbias", dbias, torch.float32, (E, N), dev)
+    else:
+        dbias = None
+    if workspace is None:
+        workspace = _empty((max(moe_matmul_grad_workspace_bytes(R, E, N, K), 1),), torch.uint8, dev,
+                           stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs contiguous memory on {dev}")
+    address = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    code = lambda t: MOE_F32 if t is None else _dtype_code(t)  # noqa: E731
+    _enqueue("moe_expert_matmul_grad", dev, stream, _arg("dy", dy, torch.bfloat16, (R, N), dev),
+             _opt("a", a, torch.bfloat16, (A, K), dev), A,
+             _opt("row_token", row_token, torch.int32, (R,), dev),
+             _arg("w", w, torch.bfloat16, (E, N, K), dev),
+             _opt("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev), R, E, N, K,
+             MAT_ACT_CODES[act], address(pre), address(da), code(da), address(dw), code(dw),
+             address(dbias), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    got = {"da": da, "dw": dw, "dbias": dbias}
+    return tuple(got[name] for name in want)

@@ -7,7 +7,8 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "moe_route.hip")
-LAYER_SRCS = [os.path.join(PKG, "csrc", name) for name in ("moe_balance.hip", "moe_experts.hip")]
+LAYER_SRCS = [os.path.join(PKG, "csrc", name) for name in (
+    "moe_balance.hip", "moe_experts.hip", "moe_gate.hip", "moe_matmul.hip", "moe_combine_grad.hip")]
 LIB = os.path.join(PKG, "libmoe_route.so")
 BENCH_SRC = os.path.join(PKG, "csrc", "bench_copy.hip")
 BENCH_LIB = os.path.join(PKG, "libmoe_bench_copy.so")

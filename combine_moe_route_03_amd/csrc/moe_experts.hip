@@ -23,6 +23,8 @@ using namespace moe_dev;
 // for an element. G lanes take a row, with up to NV vectors of 8 elements a lane in flight at once.
 // Rows beyond 512 lanes of 8 vectors are read a second time, from the cache.
 constexpr int kQuantVec = 8;
+constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
+constexpr int kCus = 256;
 
 // Eight elements as they are in memory.
 struct Bf16x8 {

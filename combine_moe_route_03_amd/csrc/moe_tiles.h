@@ -15,9 +15,6 @@
 
 namespace moe_dev {
 
-constexpr int kXcds = 8;                 // workgroup b runs on XCD b % 8
-constexpr int kCus = 256;
-
 // Rows [row0, row0 + rows) of expert e, channel block n; rows = 0: nothing to do.
 struct Tile {
     int32_t e, row0, rows, n;

@@ -1,0 +1,480 @@
+"""GPU tests of the operators of include/moe_block.h against their plain 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as ref
+from combine_moe_route_03_amd import _lib as moe
+from gpu_util import to_host
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _announce(msg):
+    print(f"[gpu] {msg}", flush=True)
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def off(got, want, tol, what):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} off, first {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]} for {want[bad][0]} within {tol[bad][0]}")
+
+
+# ----------------------------------------------------------------------------- scored routing --
+ROUTES = [
+    # T, E, k, groups, kept, top
+    (1, 1, 1, 1, 1, 1), (1, 8, 8, 1, 1, 1), (5, 7, 3, 1, 1, 1), (33, 16, 2, 4, 2, 2), (64, 33, 4, 3, 1, 2),
+    (130, 60, 6, 4, 2, 1), (17, 64, 8, 8, 4, 2), (70, 128, 16, 1, 1, 1), (40, 160, 6, 8, 3, 1),
+    (50, 256, 8, 8, 4, 2), (9, 384, 8, 1, 1, 1), (6, 512, 17, 16, 5, 3), (3, 1000, 64, 10, 7, 100),
+    (4, 1024, 8, 64, 3, 2), (2, 1024, 64, 1, 1, 1), (300, 4, 2, 2, 1, 2),
+]
+
+
+def check_route(logits, bias, k, score, groups, kept, top, renormalize, scale):
+    idx, w = moe.moe_route_scored(dev(logits), k, score=score, bias=None if bias is None else dev(bias),
+                                  n_groups=groups, topk_groups=kept, group_top=top,
+                                  renormalize=renormalize, scale=scale)
+    want, ww = ref.route(logits, bias, k, score, groups, kept, top, renormalize, scale)
+    assert np.array_equal(to_host(idx), want), np.argwhere(to_host(idx) != want)[0]
+    # one rounding of a value that 64 bits hold far better
+    off(f64(w), ww, np.abs(ww) * (ref.U * 1.001) + 2.0 ** -149, "weights")
+    return idx, w
+
+
+@pytest.mark.parametrize("renormalize,scale", [(True, 1.0), (False, 2.5)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,kept,top", ROUTES)
+def test_route_scored(T, E, k, groups, kept, top, score, biased, renormalize, scale):
+    _announce(f"route_scored T={T} E={E} k={k} groups={groups},{kept},{top} {score} {biased} {renormalize}")
+    rng = np.random.default_rng(T * E + k)
+    logits = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if biased else None
+    check_route(logits, bias, k, score, groups, kept, top, renormalize, scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,kept,top", [(64, 8, 1, 1, 1), (60, 6, 4, 2, 2), (256, 8, 8, 4, 2),
+                                                 (384, 20, 1, 1, 1)])
+def test_route_scored_ties(E, k, groups, kept, top, score):
+    """Equal logits and equal biases in all combinations, bf16 logits, values one step apart, and biases
+    that lift scores to within rounding of each other."""
+    _announce(f"route_scored ties E={E} k={k} groups={groups} {score}")
+    rng = np.random.default_rng(E)
+    few = rng.integers(0, 3, (40, E)).astype(np.float32)
+    coarse = torch.from_numpy(rng.standard_normal((40, E))).bfloat16().float().numpy()
+    close = np.float32(0.3) + (rng.integers(0, 4, (40, E)) * 2.0 ** -24).astype(np.float32)
+    flat = np.zeros((2, E), np.float32)
+    logits = np.concatenate([few, coarse, close, flat])
+    for bias in (None, np.zeros(E, np.float32), (rng.integers(0, 3, E) * 0.25).astype(np.float32),
+                 (rng.integers(0, 4, E) * 2.0 ** -26).astype(np.float32)):
+        check_route(logits, bias, k, score, groups, kept, top, True, 1.0)
+    # biases that make up for the scores' differences to a few units of the last place
+    l = rng.standard_normal((1, E)).astype(np.float32)
+    bias = (0.75 - ref.scores(l.astype(np.float64), score)[0]).astype(np.float32)
+    check_route(np.repeat(l, 3, 0), bias, k, score, groups, kept, top, False, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,kept,top", [(8, 8, 1, 1, 1), (60, 6, 4, 1, 2), (256, 8, 8, 2, 2)])
+def test_route_scored_masks_and_extremes(E, k, groups, kept, top, score):
+    _announce(f"route_scored masks E={E} k={k} {score}")
+    rng = np.random.default_rng(E + 1)
+    inf = np.float32(np.inf)
+    rows = [np.full(E, -inf), np.full(E, np.finfo(np.float32).min), np.zeros(E)]
+    one = np.full(E, -inf)
+    one[E // 2] = -3.0
+    half_ = rng.standard_normal(E)
+    half_[rng.random(E) < 0.6] = -inf
+    wide = rng.standard_normal(E) * 60
+    low = rng.standard_normal(E)
+    low[::3] = np.finfo(np.float32).min
+    tail = np.full(E, -inf)
+    tail[-1] = 5.0
+    logits = np.array(rows + [one, half_, wide, low, tail], dtype=np.float32)
+    bias = (rng.random(E) - 0.5).astype(np.float32)
+    for b in (None, bias):
+        check_route(logits, b, k, score, groups, kept, top, True, 1.0)
+        check_route(logits, b, k, score, groups, kept, top, False, -2.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_ids_are_valid_whatever_the_logits(score):
+    _announce(f"route_scored NaN and infinity {score}")
+    rng = np.random.default_rng(2)
+    l = rng.standard_normal((64, 60)).astype(np.float32)
+    l[rng.random(l.shape) < 0.3] = np.nan
+    l[rng.random(l.shape) < 0.2] = np.inf
+    l[rng.random(l.shape) < 0.2] = -np.inf
+    l[0] = np.nan
+    bias = rng.standard_normal(60).astype(np.float32)
+    bias[[3, 9]] = [np.inf, -np.inf]
+    for b in (None, dev(bias)):
+        for groups, kept in ((1, 1), (4, 2)):
+            idx = to_host(moe.moe_route_scored(dev(l), 7, score=score, bias=b, n_groups=groups,
+                                               topk_groups=kept, group_top=2)[0])
+            assert ((idx >= 0) & (idx < 60)).all()
+            assert all(len(set(r)) == 7 for r in idx.tolist())
+            if groups > 1:
+                assert all(len({e // 15 for e in r}) <= kept for r in idx.tolist())
+
+
+# ---------------------------------------------------------------------------------- gradients --
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("renormalize,scale", [(True, 2.5), (False, 0.5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 8, 8), (7, 7, 2), (65, 16, 4), (33, 60, 6), (130, 64, 8),
+                                   (9, 160, 6), (20, 256, 8), (5, 384, 17), (2, 513, 8), (3, 1024, 64),
+                                   (6, 4, 9)])
+def test_route_scored_grad(T, E, k, score, renormalize, scale, add):
+    _announce(f"route_scored_grad T={T} E={E} k={k} {score} {renormalize} add={add}")
+    rng = np.random.default_rng(T + E + k)
+    logits = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    idx = np.stack([rng.choice(E, k, replace=k > E) for _ in range(T)]).astype(np.int32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    extra = rng.standard_normal((T, E)).astype(np.float32) if add else None
+    got = moe.moe_route_scored_grad(dev(logits), dev(idx), dev(dw), score=score, renormalize=renormalize,
+                                    scale=scale, add=None if extra is None else dev(extra))
+    off(f64(got), *ref.scored_grad(logits, idx, dw.astype(np.float64), extra, score, renormalize, scale),
+        "dlogits")
+    if add:                                     # in place
+        d = dev(extra)
+        moe.moe_route_scored_grad(dev(logits), dev(idx), dev(dw), score=score, renormalize=renormalize,
+                                  scale=scale, add=d, dlogits=d)
+        assert torch.equal(d, got)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_grad_odd_ids_and_masks(score, renormalize):
+    """Ids out of range, repeated ids, -infinity among the chosen, far and low logits."""
+    _announce(f"route_scored_grad odd ids {score} {renormalize}")
+    rng = np.random.default_rng(8)
+    T, E, k = 8, 12, 5
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    idx = np.stack([rng.choice(E, k, replace=False) for _ in range(T)]).astype(np.int32)
+    idx[0] = [-1, E, 2 ** 31 - 1, -2 ** 31, 3]
+    idx[1] = 4
+    idx[2] = -1
+    logits[3, idx[3, 1]] = -np.inf
+    logits[4] = -np.inf
+    logits[5] *= 40
+    logits[6] -= 60
+    logits[7, idx[7]] = -200.0 + np.arange(k, dtype=np.float32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    got = f64(moe.moe_route_scored_grad(dev(logits), dev(idx), dev(dw), score=score,
+                                        renormalize=renormalize))
+    off(got, *ref.scored_grad(logits, idx, dw.astype(np.float64), None, score, renormalize, 1.0), "dlogits")
+
+
+def test_bias_update():
+    _announce("bias_update")
+    rng = np.random.default_rng(1)
+    for L, E in ((1, 1), (3, 7), (48, 256), (2, 1024)):
+        bias = rng.standard_normal((L, E)).astype(np.float32)
+        counts = rng.integers(0, 50, (L, E)).astype(np.int32)
+        counts[0] = 17
+        if L > 2:
+            counts[2] = 2 ** 31 - 1 - rng.integers(0, 2, E)
+        want = bias + np.float32(0.25) * np.sign(
+            counts.sum(1, keepdims=True, dtype=np.int64) - E * counts.astype(np.int64)).astype(np.float32)
+        got = moe.moe_bias_update(dev(bias), dev(counts), 0.25)
+        assert np.array_equal(to_host(got), want)
+        b = dev(bias)
+        assert moe.moe_bias_update(b, dev(counts), 0.25, out=b) is b and torch.equal(b, got)
+        one = moe.moe_bias_update(dev(bias[0]), dev(counts[0]), 0.25)
+        assert np.array_equal(to_host(one), want[0])
+
+
+# --------------------------------------------------------------------------- combine's gradient --
+@pytest.mark.parametrize("y_dtype", [BF16, F32])
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+@pytest.mark.parametrize("T,k,H", [(1, 1, 8), (3, 2, 64), (17, 8, 216), (5, 6, 1024), (9, 3, 1032),
+                                   (4, 8, 7168), (2, 64, 8200), (130, 4, 520), (2, 5, 20000)])
+def test_combine_grad(T, k, H, o_dtype, y_dtype):
+    _announce(f"combine_grad T={T} k={k} H={H} {o_dtype} {y_dtype}")
+    g = torch.Generator().manual_seed(T * H + k)
+    y, d = torch.randn((T * k, H), generator=g).to(y_dtype), torch.randn((T, H), generator=g).to(o_dtype)
+    w = torch.randn((T, k), generator=g)
+    row = torch.randperm(T * k, generator=g).to(torch.int32)
+    dy, dw = moe.moe_combine_grad(d.cuda(), y.cuda(), row.cuda(), w.cuda())
+    r = row.long().numpy().reshape(T, k)
+    want = f64(w)[:, :, None] * f64(d)[:, None, :]
+    off(f64(dy)[r], want, np.abs(want) * (ref.U + ref.half(y_dtype == BF16)) + ref.TINY, "dy")
+    prod = f64(y)[r] * f64(d)[:, None, :]
+    # a lane's chain of products, then 6 joins in a wavefront and 4 over wavefronts
+    off(f64(dw), prod.sum(2), np.abs(prod).sum(2) * (H / 64 + 32) * ref.U + ref.TINY, "dtopk_w")
+    only, none = moe.moe_combine_grad(d.cuda(), None, row.cuda(), w.cuda(),
+                                      dy=torch.empty_like(y, device="cuda"))
+    assert none is None and torch.equal(only, dy)
+
+
+def test_combine_grad_skips_rows_outside():
+    _announce("combine_grad rows outside")
+    T, k, H = 6, 3, 1040
+    y, d = torch.randn((T * k, H)).cuda(), torch.randn((T, H)).cuda()
+    w = torch.randn((T, k)).cuda()
+    row = torch.randperm(T * k).to(torch.int32)
+    row[[0, 5, 7, 17]] = torch.tensor([-1, T * k, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    dy = torch.full((T * k, H), 77.0, device="cuda")
+    _, dw = moe.moe_combine_grad(d, y, row.cuda(), w, dy=dy)
+    named = set(row.tolist())
+    for r in range(T * k):
+        if r not in named:
+            assert (dy[r] == 77.0).all()
+    assert (dw.view(-1)[[0, 5, 7, 17]] == 0).all() and (dw != 0).sum() == T * k - 4
+
+
+# ------------------------------------------------------------------------------------ products --
+def counts_of(kind, E, R, rng):
+    """Rows of each expert, R in all."""
+    if kind == "even":
+        c = np.full(E, R // E)
+        c[: R % E] += 1
+    elif kind == "one":
+        c = np.zeros(E, np.int64)
+        c[E // 2] = R
+    else:                                       # uneven, some experts without rows
+        p = rng.random(E) ** 4
+        p[rng.random(E) < 0.3] = 0
+        p[E - 1] += 1e-3
+        c = rng.multinomial(R, p / p.sum())
+    return c
+
+
+def bf16(rng, *shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).bfloat16()
+
+
+def make(T, k, E, N, K, gather, kind, seed=0):
+    rng = np.random.default_rng(seed)
+    R = T * k
+    offsets = np.concatenate([[0], np.cumsum(counts_of(kind, E, R, rng))]).astype(np.int32)
+    a = bf16(rng, T if gather else R, K)
+    rt = rng.permutation(np.repeat(np.arange(T), k)).astype(np.int32) if gather else None
+    return rng, R, offsets, a, rt
+
+
+def run_product(a, w, offsets, rt, plain=False, **kw):
+    return moe.moe_expert_matmul(a.cuda(), w.cuda(), None if plain else dev(offsets),
+                                 row_token=None if rt is None else dev(rt),
+                                 **{n: v.cuda() if isinstance(v, torch.Tensor) else v for n, v in kw.items()})
+
+
+def check_product(T, k, E, N, K, gather, kind, act, dtype, bias, residual, pre, plain=False, offsets=None,
+                  rt=None, seed=0):
+    rng, R, o, a, r = make(T, k, E, N, K, gather, kind, seed)
+    offsets, rt = o if offsets is None else offsets(o), r if rt is None else rt(r)
+    n_w = 2 * N if act == "swiglu" else N
+    w = bf16(rng, E, n_w, K, scale=K ** -0.5)
+    b = torch.from_numpy(rng.standard_normal((E, n_w)).astype(np.float32)) if bias else None
+    res = torch.from_numpy(rng.standard_normal((R, N)).astype(np.float32)).to(dtype) if residual else None
+    out = torch.full((R, N), 12345.0, dtype=dtype, device="cuda")
+    p = torch.full((R, n_w), 12345.0, dtype=BF16, device="cuda") if pre else None
+    run_product(a, w, offsets, rt, plain, bias=b, act=act, residual=res, pre=p, out=out)
+    want, tol, wp, tp, done = ref.product(f64(a), f64(w), offsets, rt, None if b is None else f64(b), act,
+                                          None if res is None else f64(res), dtype == BF16)
+    off(f64(out)[done], want[done], tol[done], "out")
+    left = float(torch.tensor(12345.0, dtype=dtype))
+    assert (f64(out)[~done] == left).all()
+    if pre:
+        off(f64(p)[done], wp[done], tp[done], "pre")
+        assert (f64(p)[~done] == float(torch.tensor(12345.0, dtype=BF16))).all()
+    if residual:                                # the residual in place
+        x = res.cuda()
+        run_product(a, w, offsets, rt, plain, bias=b, act=act, residual=x, out=x)
+        assert torch.equal(x[torch.from_numpy(done).cuda()], out[torch.from_numpy(done).cuda()])
+
+
+SHAPES = [
+    # T, k, E, N, K, kind: one token to many, tiles that end inside, odd channels
+    (1, 1, 1, 16, 8, "even"), (1, 1, 1, 1, 64, "even"), (1, 2, 4, 40, 80, "uneven"),
+    (3, 2, 8, 33, 128, "uneven"), (16, 1, 1, 64, 72, "even"), (17, 1, 1, 130, 136, "even"),
+    (40, 4, 8, 7, 520, "uneven"), (64, 2, 60, 96, 256, "uneven"), (65, 1, 2, 200, 200, "one"),
+    (128, 8, 256, 48, 128, "uneven"), (100, 3, 5, 264, 1032, "uneven"),
+    (300, 2, 3, 520, 104, "uneven"), (700, 1, 1, 300, 320, "even"), (513, 2, 2, 257, 64, "even"),
+    (1100, 1, 4, 640, 80, "one"), (40, 8, 1024, 20, 24, "uneven"),
+]
+
+
+@pytest.mark.parametrize("act,dtype", [("none", F32), ("none", BF16), ("swiglu", F32), ("swiglu", BF16),
+                                       ("relu", F32), ("silu", BF16), ("gelu", F32)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,k,E,N,K,kind", SHAPES)
+def test_expert_matmul(T, k, E, N, K, kind, gather, act, dtype):
+    _announce(f"bf16 matmul T={T} k={k} E={E} N={N} K={K} {kind} gather={gather} {act} {dtype}")
+    n = T + N + K
+    check_product(T, k, E, N, K, gather, kind, act, dtype, n % 2 == 0, n % 3 != 0, n % 5 < 3, seed=n)
+
+
+# Enough tiles for every tile shape, persistent workgroups that take several tiles, K of one step, two,
+# three and more, whole and ragged, channels that fill no block and rows of out off 16 bytes.
+TILE_SHAPES = [
+    (1100, 4, 1100, 24, "uneven", "none"), (350, 64, 520, 40, "uneven", "swiglu"),
+    (1024, 1, 2056, 1032, "even", "none"), (2000, 40, 1000, 104, "uneven", "none"),
+    (2000, 40, 996, 168, "uneven", "swiglu"), (1024, 1, 4096, 512, "even", "gelu"),
+    (1700, 20, 1100, 456, "uneven", "swiglu"), (2600, 40, 1100, 456, "uneven", "none"),
+    (4096, 2, 2048, 32, "uneven", "none"), (3000, 1, 2049, 72, "even", "swiglu"),
+    (9000, 2, 1536, 64, "uneven", "none"), (3000, 3, 1028, 136, "one", "swiglu"),
+    (6000, 2, 1028, 200, "uneven", "swiglu"), (12000, 3, 1000, 192, "uneven", "none"),
+    (6000, 2, 4100, 200, "uneven", "silu"),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,E,N,K,kind,act", TILE_SHAPES)
+def test_expert_matmul_tiles(T, E, N, K, kind, act, gather, dtype):
+    _announce(f"bf16 matmul tiles T={T} E={E} N={N} K={K} {kind} {act} gather={gather} {dtype}")
+    n = T + E + K
+    check_product(T, 1, E, N, K, gather, kind, act, dtype, n % 2 == 0, n % 3 == 0, n % 5 < 3, seed=n)
+
+
+@pytest.mark.parametrize("T,E,N,K", [(3, 1, 40, 64), (50, 8, 33, 72), (1100, 4, 1100, 24), (2000, 40, 1000, 104),
+                                     (2600, 40, 1100, 456), (12000, 3, 1000, 192)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_expert_matmul_leaves_rows_it_does_not_own(T, E, N, K, act):
+    """Rows behind the last expert's, and rows whose row_token is out of range."""
+    _announce(f"bf16 matmul, rows left alone T={T} E={E} N={N} K={K} {act}")
+
+    def spoil(rt):
+        rt[[0, T // 4, T // 2, T - 1]] = [-1, T, 2 ** 31 - 1, -2 ** 31]
+        return rt
+
+    check_product(T, 1, E, N, K, True, "uneven", act, BF16, True, False, True,
+                  offsets=lambda o: np.minimum(o, T - T // 3).astype(np.int32), rt=spoil, seed=N)
+
+
+def test_expert_matmul_plain():
+    _announce("bf16 matmul without offsets")
+    for T, N, K in ((1, 96, 256), (5, 60, 1024), (70, 384, 512), (2000, 512, 72)):
+        check_product(T, 1, 1, N, K, False, "even", "none", F32, True, True, False, plain=True)
+
+
+def test_expert_matmul_masked_places():
+    """NaN and infinities in rows and channels that a result does not read: only what they belong to
+    has them."""
+    _announce("bf16 matmul NaN in other rows")
+    for T, E, N, K in ((4, 2, 24, 72), (40, 4, 40, 136), (700, 3, 300, 200), (5000, 2, 260, 72)):
+        rng, R, o, a, rt = make(T, 1, E, N, K, True, "even")
+        w = bf16(rng, E, N, K)
+        clean = run_product(a, w, o, rt)
+        a2, w2 = a.clone(), w.clone()
+        a2[0], w2[1, 3] = float("nan"), float("inf")
+        got = run_product(a2, w2, o, rt)
+        e = np.searchsorted(o[1:], np.arange(R), side="right")
+        row = torch.from_numpy((rt == 0)).cuda()
+        col = torch.from_numpy(e == 1).cuda()
+        assert torch.isnan(got[row]).all()
+        rest = got[~row].clone()
+        same = clean[~row].clone()
+        hit = torch.zeros_like(rest, dtype=torch.bool)
+        hit[:, 3] = col[~row]
+        assert not torch.isfinite(rest[hit]).any() and torch.equal(rest[~hit], same[~hit])
+
+
+# ---------------------------------------------------------------------- gradients of products --
+def check_grad(T, k, E, N, K, gather, kind, act, da_dtype, dw_dtype, plain=False, offsets=None, rt=None,
+               seed=0):
+    rng, R, o, a, r = make(T, k, E, N, K, gather, kind, seed)
+    offsets, rt = o if offsets is None else offsets(o), r if rt is None else rt(r)
+    w, dy = bf16(rng, E, N, K, scale=N ** -0.5), bf16(rng, R, N)
+    n_a = 2 * K if act == "swiglu" else K
+    pre = None if act == "none" else bf16(rng, R, n_a, scale=2.0)
+    da = torch.full((R, n_a), 12345.0, dtype=da_dtype, device="cuda")
+    want = ("dbias", "dw", "da")
+    got = moe.moe_expert_matmul_grad(dy.cuda(), a.cuda(), w.cuda(), None if plain else dev(offsets), want=want,
+                                     row_token=None if rt is None else dev(rt), act=act,
+                                     pre=None if pre is None else pre.cuda(), da=da, dw_dtype=dw_dtype)
+    ok, done = ref.product_grad(f64(dy), f64(a), f64(w), offsets, rt, act, None if pre is None else f64(pre),
+                                da_dtype == BF16, dw_dtype == BF16)
+    for name, t in zip(want, got):
+        value, tol = ok[name]
+        t = f64(t)
+        if name == "da":
+            assert (t[~done] == float(torch.tensor(12345.0, dtype=da_dtype))).all()
+            t, value, tol = t[done], value[done], tol[done]
+        off(t, value, tol, name)
+    # each alone gives the same
+    for name, t in zip(want, got):
+        alone, = moe.moe_expert_matmul_grad(dy.cuda(), a.cuda(), w.cuda(), None if plain else dev(offsets),
+                                            want=name, row_token=None if rt is None else dev(rt), act=act,
+                                            pre=None if pre is None else pre.cuda(), da_dtype=da_dtype,
+                                            dw_dtype=dw_dtype)
+        if name == "da":
+            alone, t = alone[torch.from_numpy(done).cuda()], t[torch.from_numpy(done).cuda()]
+        assert torch.equal(alone, t), name
+
+
+GRAD_SHAPES = [
+    (1, 1, 1, 16, 8, "even"), (1, 1, 1, 8, 64, "even"), (1, 2, 4, 40, 80, "uneven"), (3, 2, 8, 32, 128, "uneven"),
+    (17, 1, 1, 136, 264, "even"), (40, 4, 8, 8, 520, "uneven"), (64, 2, 60, 96, 256, "uneven"),
+    (65, 1, 2, 200, 200, "one"), (100, 3, 5, 264, 1032, "uneven"), (300, 2, 3, 520, 104, "uneven"),
+    (700, 1, 1, 304, 320, "even"), (513, 2, 2, 256, 64, "even"), (1100, 1, 4, 640, 80, "one"),
+    (40, 8, 1024, 24, 24, "uneven"), (3000, 1, 2, 1032, 520, "uneven"), (129, 1, 1, 2056, 1032, "even"),
+]
+
+
+@pytest.mark.parametrize("act,da_dtype,dw_dtype", [("none", F32, F32), ("swiglu", BF16, F32), ("relu", F32, BF16),
+                                                   ("silu", BF16, BF16), ("gelu", F32, F32)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,k,E,N,K,kind", GRAD_SHAPES)
+def test_expert_matmul_grad(T, k, E, N, K, kind, gather, act, da_dtype, dw_dtype):
+    _announce(f"bf16 grad T={T} k={k} E={E} N={N} K={K} {kind} gather={gather} {act} {da_dtype} {dw_dtype}")
+    check_grad(T, k, E, N, K, gather, kind, act, da_dtype, dw_dtype, seed=T + N + K)
+
+
+@pytest.mark.parametrize("T,E,N,K", [(5, 2, 16, 24), (50, 8, 40, 72), (1100, 4, 264, 136), (2000, 40, 104, 264)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_expert_matmul_grad_rows_it_does_not_own(T, E, N, K, act):
+    _announce(f"bf16 grad, rows left out T={T} E={E} N={N} K={K} {act}")
+
+    def spoil(rt):
+        rt[[0, T // 4, T // 2, T - 1]] = [-1, T, 2 ** 31 - 1, -2 ** 31]
+        return rt
+
+    check_grad(T, 1, E, N, K, True, "uneven", act, BF16, F32,
+               offsets=lambda o: np.minimum(o, T - T // 3).astype(np.int32), rt=spoil, seed=N)
+
+
+def test_expert_matmul_grad_masked_places():
+    """dy and rows that are left out may hold NaN: behind the last expert's rows, and where row_token is
+    out of range; other rows' NaN stays theirs in da."""
+    _announce("bf16 grad NaN in rows left out")
+    for T, E, N, K in ((6, 2, 24, 72), (70, 4, 40, 136), (700, 3, 296, 200)):
+        rng, R, o, a, rt = make(T, 1, E, N, K, True, "even")
+        w, dy = bf16(rng, E, N, K), bf16(rng, R, N)
+        o = np.minimum(o, R - 2).astype(np.int32)
+        rt[1], rt[R // 2] = -1, T
+        args = (a.cuda(), w.cuda(), dev(o))
+        want = ("dw", "dbias", "da")
+        clean = moe.moe_expert_matmul_grad(dy.cuda(), *args, want=want, row_token=dev(rt), da_dtype=F32)
+        dy[[1, R // 2, R - 2, R - 1]] = float("nan")
+        got = moe.moe_expert_matmul_grad(dy.cuda(), *args, want=want, row_token=dev(rt), da_dtype=F32)
+        assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+        mine = np.ones(R, bool)
+        mine[[1, R // 2, R - 2, R - 1]] = False
+        m = torch.from_numpy(mine).cuda()
+        assert torch.equal(got[2][m], clean[2][m])
+
+
+def test_expert_matmul_grad_without_rows():
+    _announce("bf16 grad without rows")
+    w = torch.randn((3, 16, 24)).bfloat16().cuda()
+    dy, a = torch.empty((0, 16), dtype=BF16, device="cuda"), torch.empty((0, 24), dtype=BF16, device="cuda")
+    o = torch.zeros(4, dtype=torch.int32, device="cuda")
+    dw, db, da = moe.moe_expert_matmul_grad(dy, a, w, o, want=("dw", "dbias", "da"))
+    assert not dw.any() and not db.any() and da.shape == (0, 24)
+    out = moe.moe_expert_matmul(a, w, o)
+    assert out.shape == (0, 16)
