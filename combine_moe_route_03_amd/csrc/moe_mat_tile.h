@@ -42,6 +42,7 @@ struct MatArgs {
     int32_t max_tiles;         // row tiles, at most
     double inv_blocks;         // 1 / n_blocks
     int32_t m_blocks;          // weights: tiles of an expert over M
+    int32_t splits;            // gradients: parts that a sum is made in, each a result of its own
 };
 
 // Rows of expert e and the first of them, as expert_rows() of the other products, which the tiles'
@@ -145,9 +146,22 @@ __device__ __forceinline__ int thread_here()
 // ---- tiles ----
 struct Work {
     Tile t;                    // weights: row0 is a row of the expert's result
-    int32_t steps;
+    int32_t step0, step1;      // steps of the sum
+    int32_t split;
     int32_t first, count;      // weights: the expert's rows
 };
+
+// The steps of part `split` of a sum of `steps`, which may be fewer than the parts.
+__device__ __forceinline__ void part_of(const MatArgs& p, int32_t split, int32_t steps, Work* w)
+{
+    w->split = split;
+    w->step0 = p.splits > 1 ? (int32_t)((int64_t)steps * split / p.splits) : 0;
+    w->step1 = p.splits > 1 ? (int32_t)((int64_t)steps * (split + 1) / p.splits) : steps;
+    if (w->step1 <= w->step0) {                               // nothing: a step behind the end, zeros
+        w->step0 = steps;
+        w->step1 = steps + 1;
+    }
+}
 
 // Tile `at` of the experts' weights: expert by expert, four blocks of M by all blocks of N at a time,
 // those of M fastest, so that tiles that run together on an XCD share their operands in its L2.
@@ -155,6 +169,8 @@ template <int BM>
 __device__ __forceinline__ Work weights_at(const MatArgs& p, int32_t at)
 {
     Work w;
+    const int32_t all = p.max_tiles * p.n_blocks, split = p.splits > 1 ? at / all : 0;
+    at -= split * all;
     const int32_t row = quotient(at, p.n_blocks, p.inv_blocks);
     w.t.e = __builtin_amdgcn_readfirstlane(row / p.m_blocks);
     const int32_t local = at - w.t.e * p.m_blocks * p.n_blocks;
@@ -167,7 +183,7 @@ __device__ __forceinline__ Work weights_at(const MatArgs& p, int32_t at)
     w.t.rows = min(BM, p.M - block * BM);
     w.count = __builtin_amdgcn_readfirstlane(expert_rows(p, w.t.e, &w.first));
     w.first = __builtin_amdgcn_readfirstlane(w.first);
-    w.steps = max(1, (w.count + 63) / 64);
+    part_of(p, split, (w.count + 63) / 64, &w);
     return w;
 }
 
@@ -322,17 +338,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // workgroup b runs on XCD b % 8: each XCD takes a run of consecutive tiles, all of them, or, where
     // the experts' rows make tiles unequal, of those that run at a time
-    int32_t first, last, stride;
+    int32_t first, last, stride, all = 0;                     // all: tiles of a part
     if (MODE == kWeightsBack) {
-        last = p.max_tiles * p.n_blocks;
+        last = p.max_tiles * p.n_blocks * p.splits;
         stride = gridDim.x;
         first = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
     } else {
-        const int32_t all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
-        const int32_t share = (all + kXcds - 1) / kXcds;
+        all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
+        const int32_t whole = all * (MODE == kRowsBack ? p.splits : 1);
+        const int32_t share = (whole + kXcds - 1) / kXcds;
         stride = gridDim.x / kXcds;
         first = (blockIdx.x % kXcds) * share + blockIdx.x / kXcds;
-        last = min((int32_t)(blockIdx.x % kXcds + 1) * share, all);
+        last = min((int32_t)(blockIdx.x % kXcds + 1) * share, whole);
     }
     if (first >= last)
         return;
@@ -376,9 +393,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         if (MODE == kWeightsBack) {
             lw = weights_at<BM>(p, load_tile);
         } else {
-            lw.t = tile_at<BM, kGroup>(p, s_prefix, load_tile);
-            lw.steps = (p.D + 63) / 64;
+            const int32_t split = MODE == kRowsBack && p.splits > 1 ? load_tile / all : 0;
+            lw.t = tile_at<BM, kGroup>(p, s_prefix, load_tile - split * all);
+            if (MODE == kRowsBack) {
+                part_of(p, split, (p.D + 63) / 64, &lw);
+            } else {
+                lw.split = lw.step0 = 0;
+                lw.step1 = (p.D + 63) / 64;
+            }
         }
+        load_step = lw.step0;
         if (tid == 0)
             s_work[load_nth % kRing] = lw;
         ++load_nth;
@@ -436,7 +460,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         if (!some)
             return;
         if (MODE == kWeightsBack) {
-            const int32_t r0 = load_step * 64, left = min(64, lw.count - r0);
+            const int32_t r0 = load_step * 64, left = max(0, min(64, lw.count - r0));
             const int64_t row = (int64_t)lw.first + r0;
             abuf = buffer_of(p.rows + row * p.M, (uint32_t)left * (uint32_t)p.M * 2u);
             wbuf = p.row_token ? buffer_of(p.cols, (uint32_t)((int64_t)p.a_rows * p.N * 2))
@@ -473,12 +497,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
             // the tokens are waited for here, before the loads, with two stages in every step: what is
             // under way from memory has come then, and the compiler does not wait again where it
             // cannot tell
-            if (STAGES == 2 || load_step == 0) {
+            if (STAGES == 2 || load_step == lw.step0) {
 #pragma unroll
                 for (int i = 0; i < kLoadsA; ++i)
                     asm volatile("" : "+v"(arow[i]));
             }
-            if (load_step == 0) {
+            if (load_step == lw.step0) {
 #pragma unroll
                 for (int i = 0; i < kLoadsA; ++i) {
                     int32_t r = arow[i];
@@ -487,7 +511,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
                     avo[i] = (uint32_t)r * (uint32_t)p.D * 2u + piece;
                 }
             }
-            ends = load_step == lw.steps - 1;                 // terms behind the sum's end are zeros
+            ends = load_step == (p.D + 63) / 64 - 1;          // terms behind the sum's end are zeros
             behind = ends && load_step * 64 + piece / 2 >= p.D;
             step_at = (uint32_t)load_step * kStepK;
             step_by = kColsAcross ? (uint32_t)load_step * 64u * (uint32_t)p.N * 2u : step_at;
@@ -513,8 +537,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         if (load_to >= lds0 + STAGES * kStage)
             load_to -= STAGES * kStage;
         ++ahead;
-        if (++load_step == lw.steps) {
-            load_step = 0;
+        if (++load_step == lw.step1) {
             load_tile += stride;
             if (load_tile < last)
                 aim();
@@ -630,14 +653,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
     ahead -= 1;
     wait_workgroup();
     for (int32_t tile = first, nth = 0; tile < last; tile += stride, ++nth) {
-        const int32_t steps = __builtin_amdgcn_readfirstlane(s_work[nth % kRing].steps);
+        const Work& work = s_work[nth % kRing];
+        const int32_t steps = __builtin_amdgcn_readfirstlane(work.step1 - work.step0);
+        const int32_t split = __builtin_amdgcn_readfirstlane(work.split);
         if (steps == 1)                                       // no wait in the loop keeps the
             wait_workgroup();                                 // tiles' rows and biases apart
         Tile t;
-        t.e = __builtin_amdgcn_readfirstlane(s_work[nth % kRing].t.e);
-        t.row0 = __builtin_amdgcn_readfirstlane(s_work[nth % kRing].t.row0);
-        t.rows = __builtin_amdgcn_readfirstlane(s_work[nth % kRing].t.rows);
-        t.n = __builtin_amdgcn_readfirstlane(s_work[nth % kRing].t.n);
+        t.e = __builtin_amdgcn_readfirstlane(work.t.e);
+        t.row0 = __builtin_amdgcn_readfirstlane(work.t.row0);
+        t.rows = __builtin_amdgcn_readfirstlane(work.t.rows);
+        t.n = __builtin_amdgcn_readfirstlane(work.t.n);
         const int32_t n0 = t.n * (SWIGLU ? BN / 2 : BN);
         // a thread's row of the tile, and its channels' biases, put into LDS at the tile's end
         const bool mine = tid < t.rows;
@@ -715,7 +740,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         // SwiGLU. Stores of whole rows count the
         // same for every wavefront, so that landed() can wait for the loads before them without them.
         const bool paired = MODE == kRowsBack && FULL && p.act == MOE_MAT_SWIGLU;
-        const int64_t row0 = MODE == kWeightsBack ? (int64_t)t.e * p.M + t.row0 : t.row0;
+        const int64_t row0 = MODE == kWeightsBack ? ((int64_t)split * p.E + t.e) * p.M + t.row0
+                                                  : (int64_t)split * p.R + t.row0;
         const Sink<OUT> out(static_cast<OUT*>(p.out), row0, t.rows, p.N, paired ? 2 : 1);
         const Sink<__bf16> pre(p.pre, row0, t.rows, p.N, SWIGLU ? 2 : 1);
         if (!out.wide || paired || (FULL && p.pre))
@@ -819,7 +845,7 @@ inline moe_status_t launch_tile(MatArgs p, hipStream_t stream)
     p.inv_blocks = 1.0 / p.n_blocks;
     p.m_blocks = MODE == kWeightsBack ? (int32_t)div_up(p.M, BM) : 0;
     const int64_t rows = MODE == kWeightsBack ? (int64_t)p.E * p.m_blocks : most_tiles(p, BM);
-    const int64_t tiles = rows * p.n_blocks;
+    const int64_t tiles = rows * p.n_blocks * p.splits;
     if (tiles > INT32_MAX / 2)
         return MOE_ERR_UNSUPPORTED;
     int64_t most = (int64_t)kCus * WGS;                       // and below 2^31 threads
@@ -865,32 +891,47 @@ constexpr TileCost kMatTiles[3][5] = {
      {128, 128, 512, 1.16f, 1.00f, 5.0f}, {0, 0, 0, 0.0f, 0.0f, 0.0f}, {0, 0, 0, 0.0f, 0.0f, 0.0f}},
 };
 
-// The shape with the least time by these figures: rounds of tiles over the slots, where an expert's
-// last tile (weights: step) is half full on average. The host knows the rows of all experts, not of each.
+// How a product is made: its tile shape, and for the gradients the parts of its sums. The least time by the
+// figures above: rounds of tiles over the slots, where an expert's last tile (weights: step) is half full
+// on average; the host knows the rows of all experts, not of each. Parts go through memory in fp32 and
+// are joined by a launch of its own, which only few tiles with long sums are worth.
+struct Plan {
+    int shape;
+    int32_t splits;
+    int64_t part_bytes;        // of all parts, 0 for one
+};
+
+constexpr int64_t kMostPartBytes = (int64_t)256 << 20;
+
 template <int MODE>
-inline int choose_tile(const MatArgs& p, int64_t n_w)
+inline Plan choose(int32_t R, int32_t E, int32_t M, int64_t n_w, int32_t D)
 {
-    const int64_t experts = p.E < p.R ? p.E : p.R;
-    int best = 0;
+    const int64_t experts = E < R ? E : R;
+    const double depth = MODE == kWeightsBack ? (double)R / E / 64 + 0.5 : (double)div_up(D, 64);
+    const int64_t bytes = (MODE == kWeightsBack ? (int64_t)E * M : (int64_t)R) * n_w * 4;
+    Plan best = {0, 1, 0};
     double least = 0.0;
-    for (int i = 0; i < 5 && kMatTiles[MODE][i].bm; ++i) {
-        const TileCost& c = kMatTiles[MODE][i];
-        int64_t tiles;
-        double steps = (double)div_up(p.D, 64);
-        if (MODE == kWeightsBack) {
-            tiles = p.E * div_up(p.M, c.bm);
-            steps = (double)p.R / p.E / 64 + 0.5;
-        } else {
-            tiles = p.offsets ? p.R / c.bm + experts / 2 : div_up(p.R, c.bm);
-            if (tiles < experts)
-                tiles = experts;
-        }
-        tiles *= div_up(n_w, c.bn);
-        const double time = (double)div_up(tiles, c.slots) *
-                            (steps * (tiles <= 256 ? c.alone : c.step) + c.tile);
-        if (i == 0 || time < least) {
-            best = i;
-            least = time;
+    for (int splits = 1; splits <= 16; splits *= 2) {
+        if (splits > 1 && (MODE == kForward || depth < 4.0 * splits || bytes * splits > kMostPartBytes))
+            break;
+        for (int i = 0; i < 5 && kMatTiles[MODE][i].bm; ++i) {
+            const TileCost& c = kMatTiles[MODE][i];
+            int64_t tiles;
+            if (MODE == kWeightsBack)
+                tiles = E * div_up(M, c.bm);
+            else if (E == 1)
+                tiles = div_up(R, c.bm);
+            else
+                tiles = R / c.bm + experts / 2 > experts ? R / c.bm + experts / 2 : experts;
+            tiles *= div_up(n_w, c.bn) * splits;
+            double time = (double)div_up(tiles, c.slots) *
+                          (depth / splits * (tiles <= 256 ? c.alone : c.step) + c.tile);
+            if (splits > 1)                                   // the join: a launch, and its bytes
+                time += 4.0 + (double)bytes * (splits + 1) / 4e6;
+            if ((splits == 1 && i == 0) || time < least) {
+                best = {i, splits, splits > 1 ? bytes * splits : 0};
+                least = time;
+            }
         }
     }
     return best;
@@ -940,6 +981,7 @@ inline MatArgs mat_args(const void* rows, const void* cols, const int32_t* row_t
     p.a_rows = a_rows;
     p.R = R;
     p.E = E;
+    p.splits = 1;
     return p;
 }
 

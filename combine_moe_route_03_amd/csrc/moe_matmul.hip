@@ -170,7 +170,7 @@ moe_status_t launch_forward(const MatArgs& p, hipStream_t stream)
             return launch_few<1, 2, 8, 4, SWIGLU, OUT>(p, stream);
         return launch_few<1, SWIGLU ? 2 : 1, 8, SWIGLU ? 4 : 2, SWIGLU, OUT>(p, stream);
     }
-    const int shape = choose_tile<kForward>(p, n_w);
+    const int shape = choose<kForward>(p.R, p.E, 0, n_w, p.D).shape;
     if (p.pre || p.extra || (!SWIGLU && p.act != MOE_MAT_NONE))
         return launch_shape<kForward, SWIGLU, true, OUT>(shape, p, stream);
     return launch_shape<kForward, SWIGLU, false, OUT>(shape, p, stream);

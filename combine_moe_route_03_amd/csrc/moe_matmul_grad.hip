@@ -7,52 +7,160 @@
 
 namespace {
 
+// ---- sums in parts ----
+// Adds up `splits` parts in order; four columns a thread. Rows of a: those of an expert, with the
+// activation's gradient; weights: all.
+template <bool ROWS, typename OUT>
+__global__ __launch_bounds__(256) void k_join_parts(MatArgs p, const f32x4* __restrict__ parts,
+                                                    int64_t total)
+{
+    const int32_t quads = p.N / 4;
+    int32_t lo = 0, hi = p.R;
+    if (ROWS && p.offsets) {
+        lo = min(max(p.offsets[0], 0), p.R);
+        hi = min(max(p.offsets[p.E], 0), p.R);
+    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / quads;
+        const int32_t n = 4 * (int32_t)(i - row * quads);
+        if (ROWS && (row < lo || row >= hi ||
+                     (p.row_token && (uint32_t)p.row_token[row] >= (uint32_t)p.a_rows)))
+            continue;
+        f32x4 y = parts[i];
+        for (int s = 1; s < p.splits; ++s)
+            y += parts[s * total + i];
+        typedef typename Four<OUT>::type four;
+        if (ROWS && p.act == MOE_MAT_SWIGLU) {
+            const __bf16* q = static_cast<const __bf16*>(p.extra) + row * 2 * p.N + n;
+            const f32x4 gate = load4(q, 4, false), up = load4(q + p.N, 4, false);
+            f32x4 z;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                z[c] = y[c] * activate(gate[c], MOE_MAT_SILU);
+                y[c] = y[c] * up[c] * slope(gate[c], MOE_MAT_SILU);
+            }
+            OUT* out = static_cast<OUT*>(p.out) + row * 2 * p.N + n;
+            *reinterpret_cast<four*>(out) = round4<OUT>(y);
+            *reinterpret_cast<four*>(out + p.N) = round4<OUT>(z);
+            continue;
+        }
+        if (ROWS && p.act != MOE_MAT_NONE) {
+            const f32x4 x = load4(static_cast<const __bf16*>(p.extra) + row * p.N + n, 4, false);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                y[c] *= slope(x[c], p.act);
+        }
+        *reinterpret_cast<four*>(static_cast<OUT*>(p.out) + 4 * i) = round4<OUT>(y);
+    }
+}
+
+template <bool ROWS, typename OUT>
+moe_status_t launch_join(const MatArgs& p, const void* parts, int64_t rows, hipStream_t stream)
+{
+    const int64_t total = rows * (p.N / 4), need = div_up(total, 256), most = 8192;
+    k_join_parts<ROWS, OUT><<<(unsigned)(need < most ? need : most), 256, 0, stream>>>(
+        p, static_cast<const f32x4*>(parts), total);
+    return launched();
+}
+
 // ---- bias gradient ----
-// Column sums of dy over an expert's rows: 16 lanes hold 128 columns, 16 rows of a workgroup at a
-// time, each lane's rows in order and the 16 joined in order.
-__global__ __launch_bounds__(256) void k_bias_grad(MatArgs p, float* __restrict__ dbias)
+// Column sums of dy over an expert's rows: 16 lanes hold 128 columns, 16 rows of a workgroup at a time and
+// four of each lane on their way, each lane's rows in order and the 16 joined in order. The rows of an
+// expert are shared out over `splits` workgroups, whose sums are joined by a launch of its own.
+__global__ __launch_bounds__(256) void k_bias_grad(MatArgs p, float* __restrict__ out)
 {
     __shared__ float s_sum[16][128];
     const int tid = threadIdx.x, g = tid & 15, slot = tid >> 4;
-    const int32_t e = blockIdx.x / p.n_blocks, n = (blockIdx.x % p.n_blocks) * 128 + 8 * g;
+    const int32_t block = blockIdx.x % p.n_blocks, part = blockIdx.x / p.n_blocks;
+    const int32_t split = part % p.splits, e = part / p.splits;
+    const int32_t n = block * 128 + 8 * g;
     int32_t lo;
     const int32_t count = expert_rows(p, e, &lo);
+    const int32_t r0 = (int32_t)((int64_t)count * split / p.splits);
+    const int32_t r1 = (int32_t)((int64_t)count * (split + 1) / p.splits);
     float sum[8] = {};
     if (n < p.N)
-        for (int32_t r = slot; r < count; r += 16) {
-            if (p.row_token && (uint32_t)p.row_token[lo + r] >= (uint32_t)p.a_rows)
-                continue;
-            const bf16x8 v = *reinterpret_cast<const bf16x8*>(p.rows + (int64_t)(lo + r) * p.N + n);
+        for (int32_t r = r0 + slot; r < r1; r += 64) {
+            bool in[4];
+            bf16x8 v[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                sum[c] += (float)v[c];
+            for (int i = 0; i < 4; ++i) {
+                in[i] = r + 16 * i < r1;
+                if (p.row_token && in[i])
+                    in[i] = (uint32_t)p.row_token[lo + r + 16 * i] < (uint32_t)p.a_rows;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (in[i])
+                    v[i] = *reinterpret_cast<const bf16x8*>(p.rows + (int64_t)(lo + r + 16 * i) * p.N + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (in[i]) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        sum[c] += (float)v[i][c];
+                }
         }
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         s_sum[slot][8 * g + c] = sum[c];
     __syncthreads();
-    const int32_t col = (blockIdx.x % p.n_blocks) * 128 + tid;
+    const int32_t col = block * 128 + tid;
     if (tid < 128 && col < p.N) {
         float all = 0.0f;
 #pragma unroll
         for (int s = 0; s < 16; ++s)
             all += s_sum[s][tid];
-        dbias[(int64_t)e * p.N + col] = all;
+        out[((int64_t)split * p.E + e) * p.N + col] = all;
     }
 }
 
-template <typename OUT>
-moe_status_t launch_rows(const MatArgs& p, hipStream_t stream)
+__global__ __launch_bounds__(256) void k_join_bias(const float* __restrict__ parts, int64_t total,
+                                                   int32_t splits, float* __restrict__ dbias)
 {
-    const int shape = choose_tile<kRowsBack>(p, p.N);
-    return p.act != MOE_MAT_NONE ? launch_shape<kRowsBack, false, true, OUT>(shape, p, stream)
-                                 : launch_shape<kRowsBack, false, false, OUT>(shape, p, stream);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        float sum = parts[i];
+        for (int s = 1; s < splits; ++s)
+            sum += parts[s * total + i];
+        dbias[i] = sum;
+    }
+}
+
+// Workgroups for the rows of an expert: four a CU in all, of 256 rows at least.
+int32_t bias_splits(int32_t R, int32_t E, int32_t N)
+{
+    int64_t s = 1024 / ((int64_t)E * div_up(N, 128));
+    if (s > (int64_t)R / E / 256)
+        s = (int64_t)R / E / 256;
+    return s < 1 ? 1 : s > 256 ? 256 : (int32_t)s;
 }
 
 template <typename OUT>
-moe_status_t launch_weights(const MatArgs& p, hipStream_t stream)
+moe_status_t launch_rows(MatArgs p, void* parts, hipStream_t stream)
 {
-    return launch_shape<kWeightsBack, false, false, OUT>(choose_tile<kWeightsBack>(p, p.N), p, stream);
+    const Plan plan = choose<kRowsBack>(p.R, p.E, 0, p.N, p.D);
+    if (plan.splits == 1)
+        return p.act != MOE_MAT_NONE ? launch_shape<kRowsBack, false, true, OUT>(plan.shape, p, stream)
+                                     : launch_shape<kRowsBack, false, false, OUT>(plan.shape, p, stream);
+    MatArgs q = p;
+    q.splits = p.splits = plan.splits;
+    q.out = parts;
+    q.act = MOE_MAT_NONE;
+    const moe_status_t st = launch_shape<kRowsBack, false, false, float>(plan.shape, q, stream);
+    return st != MOE_OK ? st : launch_join<true, OUT>(p, parts, p.R, stream);
+}
+
+template <typename OUT>
+moe_status_t launch_weights(MatArgs p, void* parts, hipStream_t stream)
+{
+    const Plan plan = choose<kWeightsBack>(p.R, p.E, p.M, p.N, 0);
+    if (plan.splits == 1)
+        return launch_shape<kWeightsBack, false, false, OUT>(plan.shape, p, stream);
+    MatArgs q = p;
+    q.splits = p.splits = plan.splits;
+    q.out = parts;
+    const moe_status_t st = launch_shape<kWeightsBack, false, false, float>(plan.shape, q, stream);
+    return st != MOE_OK ? st : launch_join<false, OUT>(p, parts, (int64_t)p.E * p.M, stream);
 }
 
 }  // namespace
@@ -61,7 +169,17 @@ extern "C" {
 
 size_t moe_matmul_grad_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K)
 {
-    return R < 0 || E < 1 || N < 1 || K < 1 ? 0 : 256;
+    if (R < 0 || E < 1 || N < 1 || K < 1)
+        return 0;
+    int64_t bytes = 256;
+    if (R > 0) {
+        const int64_t rows = choose<kRowsBack>(R, E, 0, K, N).part_bytes;
+        const int64_t weights = choose<kWeightsBack>(R, E, N, K, 0).part_bytes;
+        const int64_t splits = bias_splits(R, E, N), bias = splits > 1 ? splits * E * N * 4 : 0;
+        for (const int64_t b : {rows, weights, bias})
+            bytes = b > bytes ? b : bytes;
+    }
+    return (size_t)bytes;
 }
 
 moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_rows,
@@ -97,8 +215,8 @@ moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_row
         p.N = K;
         p.D = N;
         p.act = act;
-        st = da_dtype == MOE_BF16 ? launch_rows<__bf16>(p, stream)
-                                  : launch_rows<float>(p, stream);
+        st = da_dtype == MOE_BF16 ? launch_rows<__bf16>(p, workspace, stream)
+                                  : launch_rows<float>(p, workspace, stream);
         if (st != MOE_OK)
             return st;
     }
@@ -107,8 +225,8 @@ moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_row
         p.out = dw;
         p.N = K;
         p.M = N;
-        st = dw_dtype == MOE_BF16 ? launch_weights<__bf16>(p, stream)
-                                  : launch_weights<float>(p, stream);
+        st = dw_dtype == MOE_BF16 ? launch_weights<__bf16>(p, workspace, stream)
+                                  : launch_weights<float>(p, workspace, stream);
         if (st != MOE_OK)
             return st;
     }
@@ -116,7 +234,14 @@ moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_row
         MatArgs p = mat_args(dy, nullptr, row_token, expert_offsets, a_rows, R, E);
         p.N = N;
         p.n_blocks = (int32_t)div_up(N, 128);
-        k_bias_grad<<<(unsigned)(E * p.n_blocks), 256, 0, stream>>>(p, dbias);
+        p.splits = R > 0 ? bias_splits(R, E, N) : 1;
+        float* parts = p.splits > 1 ? static_cast<float*>(workspace) : dbias;
+        k_bias_grad<<<(unsigned)(E * p.splits * p.n_blocks), 256, 0, stream>>>(p, parts);
+        if (p.splits > 1) {
+            const int64_t total = (int64_t)E * N, need = div_up(total, 256);
+            k_join_bias<<<(unsigned)(need < 4096 ? need : 4096), 256, 0, stream>>>(parts, total, p.splits,
+                                                                                 dbias);
+        }
         st = launched();
     }
     return st;

@@ -435,7 +435,25 @@ def test_expert_matmul_grad(T, k, E, N, K, kind, gather, act, da_dtype, dw_dtype
     check_grad(T, k, E, N, K, gather, kind, act, da_dtype, dw_dtype, seed=T + N + K)
 
 
-@pytest.mark.parametrize("T,E,N,K", [(5, 2, 16, 24), (50, 8, 40, 72), (1100, 4, 264, 136), (2000, 40, 104, 264)])
+# Sums in parts: few rows with long sums of da, small weights with many rows, and experts whose rows do not
+# fill the parts.
+PART_SHAPES = [
+    (24, 1, 4096, 64, "even"), (40, 2, 2056, 136, "uneven"), (3000, 1, 64, 72, "even"),
+    (5000, 3, 40, 64, "one"), (6000, 4, 136, 64, "uneven"), (130, 1, 8200, 264, "even"),
+]
+
+
+@pytest.mark.parametrize("act,da_dtype,dw_dtype", [("none", F32, BF16), ("swiglu", BF16, F32), ("gelu", F32, F32)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,E,N,K,kind", PART_SHAPES)
+def test_expert_matmul_grad_in_parts(T, E, N, K, kind, gather, act, da_dtype, dw_dtype):
+    _announce(f"bf16 grad in parts T={T} E={E} N={N} K={K} {kind} gather={gather} {act}")
+    assert moe.moe_matmul_grad_workspace_bytes(T, E, N, K) >= 8 * min(T * K, E * N * K)
+    check_grad(T, 1, E, N, K, gather, kind, act, da_dtype, dw_dtype, seed=T + N + K)
+
+
+@pytest.mark.parametrize("T,E,N,K", [(5, 2, 16, 24), (50, 8, 40, 72), (1100, 4, 264, 136), (2000, 40, 104, 264),
+                                     (40, 2, 2056, 136), (5000, 3, 40, 64)])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_expert_matmul_grad_rows_it_does_not_own(T, E, N, K, act):
     _announce(f"bf16 grad, rows left out T={T} E={E} N={N} K={K} {act}")
@@ -452,7 +470,7 @@ def test_expert_matmul_grad_masked_places():
     """dy and rows that are left out may hold NaN: behind the last expert's rows, and where row_token is
     out of range; other rows' NaN stays theirs in da."""
     _announce("bf16 grad NaN in rows left out")
-    for T, E, N, K in ((6, 2, 24, 72), (70, 4, 40, 136), (700, 3, 296, 200)):
+    for T, E, N, K in ((6, 2, 24, 72), (70, 4, 40, 136), (700, 3, 296, 200), (40, 2, 2056, 136), (6000, 2, 40, 64)):
         rng, R, o, a, rt = make(T, 1, E, N, K, True, "even")
         w, dy = bf16(rng, E, N, K), bf16(rng, R, N)
         o = np.minimum(o, R - 2).astype(np.int32)
