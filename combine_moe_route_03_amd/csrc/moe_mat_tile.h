@@ -190,14 +190,13 @@ __device__ __forceinline__ Work weights_at(const MatArgs& p, int32_t at)
 // Results of a wavefront's fragments, row lane % 32 and columns 8 i + 4 (lane / 32) + c of fragment
 // g in v[g][i], through a little LDS of its own and out as whole lines: 16-byte piece c of row r
 // lies in slot c ^ (r % 8).
-template <typename OUT, int F>
+template <int UNIT, typename OUT, int F>
 __device__ __forceinline__ void store_unit(int8_t* unit, const typename Four<OUT>::type (&v)[F][4],
                                            OUT* base, __amdgpu_buffer_rsrc_t buffer, bool wide,
                                            int32_t ld, int32_t n_end, int32_t tr, int32_t n1,
                                            uint32_t rows, int lane)
 {
-    constexpr int kUnit = 1024;
-    constexpr int kRow = F * 32 * (int)sizeof(OUT), kRows = kUnit / kRow < 32 ? kUnit / kRow : 32;
+    constexpr int kRow = F * 32 * (int)sizeof(OUT), kRows = UNIT / kRow < 32 ? UNIT / kRow : 32;
     constexpr int kStores = kRows * kRow / 1024, kPieces = kRow / 16;
     static_assert(kStores >= 1, "unit");
     const int r32 = lane & 31, half = lane >> 5;
@@ -321,7 +320,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
     static_assert(MODE == kForward || !SWIGLU, "only the forward product pairs channels");
     static_assert(MODE != kWeightsBack || STAGES == 2, "row tokens have come with the stage before");
     // results of a wavefront: fragments side by side, and the units they are stored in
-    constexpr int kUnit = 1024;
+    constexpr int kUnit = STAGES * kStage + kWaves * 2048 + 8192 <= 163840 ? 2048 : 1024;
     constexpr int kOutF = SWIGLU ? NF / 2 : NF, kUnitF = kOutF < 2 || sizeof(OUT) == 4 ? 1 : 2;
     constexpr int kStores = MF * (kOutF / kUnitF) * kUnitF * 32 * 32 * (int)sizeof(OUT) / 1024;
     static_assert(NF == 2 && BM <= kThreads, "results");
@@ -817,16 +816,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
                         v[g][i] = round4<OUT>(y);
                     }
                 if (MODE == kForward && FULL && p.pre) {
-                    store_unit<__bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.ld, p.N,
+                    store_unit<kUnit, __bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.ld, p.N,
                                                tr, n1, rows, lane);
                     if (SWIGLU)
-                        store_unit<__bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide, pre.ld,
+                        store_unit<kUnit, __bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide, pre.ld,
                                                    n_w, tr, p.N + n1, rows, lane);
                 }
-                store_unit<OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.ld, p.N, tr, n1,
+                store_unit<kUnit, OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.ld, p.N, tr, n1,
                                         rows, lane);
                 if (MODE == kRowsBack && FULL && paired)
-                    store_unit<OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.ld, 2 * p.N,
+                    store_unit<kUnit, OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.ld, 2 * p.N,
                                             tr, p.N + n1, rows, lane);
             }
         }
