@@ -204,7 +204,7 @@ moe_status_t moe_combine_grad(const void* dout, moe_dtype_t dout_dtype, const vo
                               int32_t T, int32_t H, int32_t k, void* dy, float* dtopk_w,
                               hipStream_t stream)
 {
-    if (T < 0 || H < 1 || k < 1 || (int64_t)T * k > INT32_MAX || (!dy && !dtopk_w))
+    if (T < 0 || H < 1 || k < 1 || (int64_t)T * k > INT32_MAX || (T > 0 && !dy && !dtopk_w))
         return MOE_ERR_INVALID;
     if ((dout_dtype != MOE_F32 && dout_dtype != MOE_BF16) ||
         (y_dtype != MOE_F32 && y_dtype != MOE_BF16) || H % 8 != 0 || k > MOE_MAX_TOPK)

@@ -193,7 +193,7 @@ moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_row
     moe_status_t st = check_sizes(a_rows, row_token, expert_offsets, R, E, N, N, K, act);
     if (st != MOE_OK)
         return st;
-    if (!da && !dw && !dbias)
+    if (R > 0 && !da && !dw && !dbias)
         return MOE_ERR_INVALID;
     if (N % 8 != 0 || (da && da_dtype != MOE_F32 && da_dtype != MOE_BF16) ||
         (dw && dw_dtype != MOE_F32 && dw_dtype != MOE_BF16) ||
