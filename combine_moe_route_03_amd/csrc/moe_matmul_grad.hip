@@ -65,10 +65,11 @@ moe_status_t launch_join(const MatArgs& p, const void* parts, int64_t rows, hipS
 
 // ---- bias gradient ----
 // Column sums of dy over an expert's rows: 16 lanes hold 128 columns, 16 rows of a workgroup at a time and
-// four of each lane on their way, each lane's rows in order and the 16 joined in order. The rows of an
+// eight of each lane on their way, each lane's rows in order and the 16 joined in order. The rows of an
 // expert are shared out over `splits` workgroups, whose sums are joined by a launch of its own.
 __global__ __launch_bounds__(256) void k_bias_grad(MatArgs p, float* __restrict__ out)
 {
+    constexpr int kFlight = 8;
     __shared__ float s_sum[16][128];
     const int tid = threadIdx.x, g = tid & 15, slot = tid >> 4;
     const int32_t block = blockIdx.x % p.n_blocks, part = blockIdx.x / p.n_blocks;
@@ -80,21 +81,21 @@ __global__ __launch_bounds__(256) void k_bias_grad(MatArgs p, float* __restrict_
     const int32_t r1 = (int32_t)((int64_t)count * (split + 1) / p.splits);
     float sum[8] = {};
     if (n < p.N)
-        for (int32_t r = r0 + slot; r < r1; r += 64) {
-            bool in[4];
-            bf16x8 v[4];
+        for (int32_t r = r0 + slot; r < r1; r += 16 * kFlight) {
+            bool in[kFlight];
+            bf16x8 v[kFlight];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kFlight; ++i) {
                 in[i] = r + 16 * i < r1;
                 if (p.row_token && in[i])
                     in[i] = (uint32_t)p.row_token[lo + r + 16 * i] < (uint32_t)p.a_rows;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kFlight; ++i)
                 if (in[i])
                     v[i] = *reinterpret_cast<const bf16x8*>(p.rows + (int64_t)(lo + r + 16 * i) * p.N + n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kFlight; ++i)
                 if (in[i]) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
