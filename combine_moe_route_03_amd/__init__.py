@@ -16,7 +16,8 @@ _EXPORTS = ("moe_route_topk", "moe_dispatch_workspace_bytes", "moe_dispatch_layo
             "moe_ep_combine_reduced", "moe_check_topk", "moe_balance_workspace_bytes",
             "alloc_balance_workspace", "moe_balance_loss", "moe_route_grad", "moe_quant_rows",
             "moe_expert_matmul_i8", "moe_route_scored", "moe_route_scored_grad", "moe_bias_update",
-            "moe_combine_grad", "moe_expert_matmul", "moe_expert_matmul_grad",
+            "moe_combine_grad", "moe_expert_matmul", "moe_expert_matmul_workspace_bytes",
+            "alloc_expert_matmul_workspace", "moe_expert_matmul_grad",
             "moe_matmul_grad_workspace_bytes", "alloc_matmul_grad_workspace")
 
 

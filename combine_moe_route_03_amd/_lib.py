@@ -95,7 +95,9 @@ def load() -> ctypes.CDLL:
         lib.moe_route_scored_grad.argtypes = [P, P, P, P, I, I, I, I, I, F, P, P]
         lib.moe_bias_update.argtypes = [P, P, I, I, F, P, P]
         lib.moe_combine_grad.argtypes = [P, I, P, I, P, P, I, I, I, P, P, P]
-        lib.moe_expert_matmul.argtypes = [P, I, P, P, P, P, I, I, I, I, I, P, P, P, I, P]
+        lib.moe_expert_matmul_workspace_bytes.argtypes = [I, I, I, I]
+        lib.moe_expert_matmul_workspace_bytes.restype = Z
+        lib.moe_expert_matmul.argtypes = [P, I, P, P, P, P, I, I, I, I, I, P, P, P, I, P, Z, P]
         lib.moe_matmul_grad_workspace_bytes.argtypes = [I, I, I, I]
         lib.moe_matmul_grad_workspace_bytes.restype = Z
         lib.moe_expert_matmul_grad.argtypes = [P, P, I, P, P, P, I, I, I, I, I, P, P, I, P, I, P, P, Z,
@@ -728,19 +730,33 @@ def _product_sizes(w: torch.Tensor, act: str, R: int):
     return E, n_w, K
 
 
+@functools.lru_cache(maxsize=1024)
+def moe_expert_matmul_workspace_bytes(R: int, E: int, channels: int, K: int) -> int:
+    if max(R, E, channels, K) > _MOST:
+        _too_large("R, E, channels, K", R, E, channels, K)
+    return int(load().moe_expert_matmul_workspace_bytes(R, E, channels, K))
+
+
+def alloc_expert_matmul_workspace(R: int, E: int, channels: int, K: int, device="cuda") -> torch.Tensor:
+    n = max(moe_expert_matmul_workspace_bytes(R, E, channels, K), 1)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def moe_expert_matmul(a: torch.Tensor, w: torch.Tensor,
                       expert_offsets: Optional[torch.Tensor] = None,
                       row_token: Optional[torch.Tensor] = None,
                       bias: Optional[torch.Tensor] = None, act: str = "none",
                       residual: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
                       out: Optional[torch.Tensor] = None,
-                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+                      out_dtype: torch.dtype = torch.bfloat16,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The experts' product of bf16 rows a [A,K] with bf16 weights w [E,N,K] (act "swiglu": [E,2N,K],
     gate channels first): act(a w^T + bias) + residual, out [R,N] in out's type or out_dtype. act is
     "none", "relu", "silu", "gelu" (tanh form) or "swiglu"; bias [E,N or 2N] fp32; residual [R,N] in
     out's type, it may be out; pre [R,N or 2N] bf16 gets the sums before the activation. Row r of expert
     e (expert_offsets [E+1]) reads row row_token[r] of a, or row r without row_token. Without
-    expert_offsets E must be 1: a plain product."""
+    expert_offsets E must be 1: a plain product. Sizes that need a workspace and get none have one
+    allocated for the call."""
     dev, A, K = _matrix("a", a)
     R = A if row_token is None else row_token.numel()
     E, n_w, _ = _product_sizes(w, act, R)
@@ -749,6 +765,11 @@ def moe_expert_matmul(a: torch.Tensor, w: torch.Tensor,
     N = n_w // 2 if act == "swiglu" else n_w
     if out is None:
         out = _empty((R, N), out_dtype, dev, stream)
+    if workspace is None:
+        need = moe_expert_matmul_workspace_bytes(R, E, n_w, K)
+        workspace = _empty((need,), torch.uint8, dev, stream) if need else None
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs contiguous memory on {dev}")
     _enqueue("moe_expert_matmul", dev, stream, _arg("a", a, torch.bfloat16, (A, K), dev), A,
              _opt("row_token", row_token, torch.int32, (R,), dev),
              _arg("w", w, torch.bfloat16, (E, n_w, K), dev),
@@ -756,7 +777,9 @@ def moe_expert_matmul(a: torch.Tensor, w: torch.Tensor,
              _opt("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev), R, E, N, K,
              MAT_ACT_CODES[act], _opt("residual", residual, out.dtype, (R, N), dev),
              _opt("pre", pre, torch.bfloat16, (R, n_w), dev),
-             _arg("out", out, _WIDE, (R, N), dev), _dtype_code(out))
+             _arg("out", out, _WIDE, (R, N), dev), _dtype_code(out),
+             None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
 
 

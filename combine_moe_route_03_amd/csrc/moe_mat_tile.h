@@ -42,7 +42,7 @@ struct MatArgs {
     int32_t max_tiles;         // row tiles, at most
     double inv_blocks;         // 1 / n_blocks
     int32_t m_blocks;          // weights: tiles of an expert over M
-    int32_t splits;            // gradients: parts that a sum is made in, each a result of its own
+    int32_t splits;            // parts that a sum is made in, each a result of its own
 };
 
 // Rows of expert e and the first of them, as expert_rows() of the other products, which the tiles'
@@ -247,6 +247,20 @@ __device__ __forceinline__ void store_unit(int8_t* unit, const typename Four<OUT
     }
 }
 
+// `left` of four values at p (or all, if more).
+template <typename OUT>
+__device__ __forceinline__ void store4(OUT* p, typename Four<OUT>::type v, int32_t left)
+{
+    if (left >= 4 && (uintptr_t)p % sizeof(v) == 0) {
+        *reinterpret_cast<typename Four<OUT>::type*>(p) = v;
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c < left)
+                p[c] = v[c];
+    }
+}
+
 template <typename OUT>
 __device__ __forceinline__ typename Four<OUT>::type round4(f32x4 y)
 {
@@ -347,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         first = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
     } else {
         all = tile_prefix<kThreads, BM>(p, s_prefix) * p.n_blocks;
-        const int32_t whole = all * (MODE == kRowsBack ? p.splits : 1);
+        const int32_t whole = all * p.splits;
         const int32_t share = (whole + kXcds - 1) / kXcds;
         stride = gridDim.x / kXcds;
         first = (blockIdx.x % kXcds) * share + blockIdx.x / kXcds;
@@ -395,14 +409,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         if (MODE == kWeightsBack) {
             lw = weights_at<BM>(p, load_tile);
         } else {
-            const int32_t split = MODE == kRowsBack && p.splits > 1 ? load_tile / all : 0;
+            const int32_t split = p.splits > 1 ? load_tile / all : 0;
             lw.t = tile_at<BM, kGroup>(p, s_prefix, load_tile - split * all);
-            if (MODE == kRowsBack) {
-                part_of(p, split, (p.D + 63) / 64, &lw);
-            } else {
-                lw.split = lw.step0 = 0;
-                lw.step1 = (p.D + 63) / 64;
-            }
+            part_of(p, split, (p.D + 63) / 64, &lw);
         }
         load_step = lw.step0;
         if (tid == 0)
@@ -893,7 +902,7 @@ constexpr TileCost kMatTiles[3][5] = {
      {128, 128, 512, 1.16f, 1.00f, 5.0f}, {0, 0, 0, 0.0f, 0.0f, 0.0f}, {0, 0, 0, 0.0f, 0.0f, 0.0f}},
 };
 
-// How a product is made: its tile shape, and for the gradients the parts of its sums. The least time by the
+// How a product is made: its tile shape, and the parts of its sums. The least time by the
 // figures above: rounds of tiles over the slots, where an expert's last tile (weights: step) is half full
 // on average; the host knows the rows of all experts, not of each. Parts go through memory in fp32 and
 // are joined by a launch of its own, which only few tiles with long sums are worth.
@@ -914,7 +923,7 @@ inline Plan choose(int32_t R, int32_t E, int32_t M, int64_t n_w, int32_t D)
     Plan best = {0, 1, 0};
     double least = 0.0;
     for (int splits = 1; splits <= 16; splits *= 2) {
-        if (splits > 1 && (MODE == kForward || depth < 4.0 * splits || bytes * splits > kMostPartBytes))
+        if (splits > 1 && (depth < 4.0 * splits || bytes * splits > kMostPartBytes))
             break;
         for (int i = 0; i < 5 && kMatTiles[MODE][i].bm; ++i) {
             const TileCost& c = kMatTiles[MODE][i];

@@ -6,19 +6,18 @@
 namespace {
 
 // ---- few rows ----
-// Bound by reading the weights, each once: a workgroup takes up to 16 MF rows of one expert and 16 NF
+// Bound by reading the weights, each once: a workgroup takes up to 16 rows of one expert and 16 NF
 // channels; its wavefronts share the sum out by 128-byte pieces, read weights and rows straight into
 // operands, and add their fp32 sums up through LDS, in wavefront order. v_mfma_f32_16x16x32_bf16 with
 // the weights as the left operand: lane l gives channel l % 16 and 16 bytes of the sum at 16 (l / 16),
 // and gets row l % 16 with channels 4 (l / 16) + i.
-template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
+template <int NF, int WAVES, int U, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
 {
-    constexpr int kFrags = MF * NF;
-    __shared__ f32x4 s_acc[WAVES][kFrags][64];
+    __shared__ f32x4 s_acc[WAVES][NF][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t nb = blockIdx.x % p.n_blocks;
-    const Tile tile = find_tile<16 * MF>(p, blockIdx.x / p.n_blocks);
+    const Tile tile = find_tile<16>(p, blockIdx.x / p.n_blocks);
     if (tile.rows == 0)
         return;
     const int r16 = lane & 15, kq = lane >> 4;
@@ -35,25 +34,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
         n = min(n, p.N - 1) + (SWIGLU && (f & 1) ? p.N : 0);
         wp[f] = we + (int64_t)n * p.D;
     }
-    const __bf16* ap[MF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-        const int32_t r = tile.row0 + min(16 * m + r16, tile.rows - 1);
-        int32_t src = p.row_token ? p.row_token[r] : r;
-        src = (uint32_t)src < (uint32_t)p.a_rows ? src : 0;   // its results are not stored
-        ap[m] = p.rows + (int64_t)src * p.D;
-    }
+    const int32_t row = tile.row0 + min(r16, tile.rows - 1);
+    const int32_t src = p.row_token ? p.row_token[row] : row;
+    const bool there = (uint32_t)src < (uint32_t)p.a_rows;    // else its results are not stored
+    const __bf16* ap = p.rows + (int64_t)(there ? src : 0) * p.D;
     // the fragment (with SwiGLU the pair) that this wavefront will join and store
     constexpr int kStep = SWIGLU ? 2 : 1;
-    static_assert(kFrags <= WAVES * kStep, "one for a wavefront");
+    static_assert(NF <= WAVES * kStep, "one for a wavefront");
     const int mine = wave * kStep;
-    const int32_t at_row = 16 * (mine / NF) + r16;
-    const int32_t row = tile.row0 + min(at_row, tile.rows - 1);
-    const int32_t src = p.row_token ? p.row_token[row] : row;
-    const int32_t n = n0 + (SWIGLU ? 8 : 16) * (mine % NF) + 4 * kq;
+    const int32_t n = n0 + (SWIGLU ? 8 : 16) * mine + 4 * kq;
     const int32_t left = p.N - n;
-    const bool stores = mine < kFrags && at_row < tile.rows &&
-                        (uint32_t)src < (uint32_t)p.a_rows && left > 0;
+    const bool stores = mine < NF && r16 < tile.rows && there && left > 0;
     const bool vec = p.N % 4 == 0;
     f32x4 b0 = {0.0f, 0.0f, 0.0f, 0.0f}, b1 = b0, res = b0;
     if (stores && p.bias) {
@@ -65,15 +56,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
     if (stores && p.extra)
         res = load4(static_cast<const OUT*>(p.extra) + (int64_t)row * p.N + n, left,
                     vec && (uintptr_t)p.extra % 16 == 0);
-    f32x4 acc[MF][NF];
+    f32x4 acc[NF];
 #pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            acc[m][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int f = 0; f < NF; ++f)
+        acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     for (int32_t k0 = wave * 64; k0 < p.D; k0 += U * WAVES * 64) {
-        bf16x8 wv[2 * U][NF], av[2 * U][MF];
+        bf16x8 wv[2 * U][NF], av[2 * U];
 #pragma unroll
         for (int h = 0; h < 2 * U; ++h) {
             const int32_t at = k0 + h / 2 * WAVES * 64 + 32 * (h % 2) + 8 * kq;
@@ -84,26 +73,18 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
                 wv[h][f] = *reinterpret_cast<const bf16x8*>(wp[f] + (in ? at : 0));
                 wv[h][f] = in ? wv[h][f] : none;
             }
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                av[h][m] = *reinterpret_cast<const bf16x8*>(ap[m] + (in ? at : 0));
-                av[h][m] = in ? av[h][m] : none;
-            }
+            av[h] = *reinterpret_cast<const bf16x8*>(ap + (in ? at : 0));
+            av[h] = in ? av[h] : none;
         }
 #pragma unroll
         for (int h = 0; h < 2 * U; ++h)
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[h][f], av[h][m],
-                                                                        acc[m][f], 0, 0, 0);
+            for (int f = 0; f < NF; ++f)
+                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[h][f], av[h], acc[f], 0, 0, 0);
     }
 #pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            s_acc[wave][m * NF + f][lane] = acc[m][f];
+    for (int f = 0; f < NF; ++f)
+        s_acc[wave][f][lane] = acc[f];
     __syncthreads();
     if (!stores)
         return;
@@ -116,21 +97,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
             sum[g] += s_acc[w][mine + g][lane];
     }
     f32x4 y = sum[0] + b0, up = sum[kStep - 1] + b1;
-    const auto put = [&](auto* to, auto v) {
-        if (left >= 4 && (uintptr_t)to % sizeof(v) == 0) {
-            *reinterpret_cast<decltype(v)*>(to) = v;
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < left)
-                    to[c] = v[c];
-        }
-    };
     if (p.pre) {
         __bf16* q = p.pre + (int64_t)row * n_w + n;
-        put(q, round4<__bf16>(y));
+        store4(q, round4<__bf16>(y), left);
         if (SWIGLU)
-            put(q + p.N, round4<__bf16>(up));
+            store4(q + p.N, round4<__bf16>(up), left);
     }
     if (SWIGLU) {
         y = swiglu(y, up);
@@ -141,50 +112,142 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
     }
     if (p.extra)
         y += res;
-    put(static_cast<OUT*>(p.out) + (int64_t)row * p.N + n, round4<OUT>(y));
+    store4(static_cast<OUT*>(p.out) + (int64_t)row * p.N + n, round4<OUT>(y), left);
 }
 
-template <int MF, int NF, int WAVES, int U, bool SWIGLU, typename OUT>
+// ---- sums in parts ----
+// Adds up `splits` parts [R, n_w] in order and does what else there is to a result: four columns of a row
+// a thread.
+template <bool SWIGLU, typename OUT>
+__global__ __launch_bounds__(256) void k_join_forward(MatArgs p, const float* __restrict__ parts)
+{
+    const int32_t quads = (p.N + 3) / 4, n_w = SWIGLU ? 2 * p.N : p.N;
+    const int64_t total = (int64_t)p.R * quads, part = (int64_t)p.R * n_w;
+    const bool vec = p.N % 4 == 0, vec_extra = vec && (uintptr_t)p.extra % 16 == 0;
+    const int32_t lo = p.offsets ? min(max(p.offsets[0], 0), p.R) : 0;
+    const int32_t hi = p.offsets ? min(max(p.offsets[p.E], 0), p.R) : p.R;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / quads;
+        const int32_t n = 4 * (int32_t)(i - row * quads), left = p.N - n;
+        if (row < lo || row >= hi ||
+            (p.row_token && (uint32_t)p.row_token[row] >= (uint32_t)p.a_rows))
+            continue;
+        const float* q = parts + row * n_w + n;
+        f32x4 y = load4(q, left, vec), z = y;
+        if (SWIGLU)
+            z = load4(q + p.N, left, vec);
+#pragma unroll 5
+        for (int s = 1; s < p.splits; ++s) {
+            y += load4(q + s * part, left, vec);
+            if (SWIGLU)
+                z += load4(q + s * part + p.N, left, vec);
+        }
+        if (p.bias) {
+            int32_t e = 0, end = p.E;                         // the row's expert
+            while (end - e > 1) {
+                const int32_t mid = (e + end) / 2;
+                if (p.offsets[mid] <= row)
+                    e = mid;
+                else
+                    end = mid;
+            }
+            const float* b = p.bias + (int64_t)e * n_w + n;
+            y += load4(b, left, false);
+            if (SWIGLU)
+                z += load4(b + p.N, left, false);
+        }
+        if (p.pre) {
+            __bf16* pre = p.pre + row * n_w + n;
+            store4(pre, round4<__bf16>(y), left);
+            if (SWIGLU)
+                store4(pre + p.N, round4<__bf16>(z), left);
+        }
+        if (SWIGLU) {
+            y = swiglu(y, z);
+        } else if (p.act != MOE_MAT_NONE) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                y[c] = activate(y[c], p.act);
+        }
+        if (p.extra)
+            y += load4(static_cast<const OUT*>(p.extra) + row * p.N + n, left, vec_extra);
+        store4(static_cast<OUT*>(p.out) + row * p.N + n, round4<OUT>(y), left);
+    }
+}
+
+template <int NF, int U, bool SWIGLU, typename OUT>
 moe_status_t launch_few(MatArgs p, hipStream_t stream)
 {
+    constexpr int kWaves = 8;
     p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
-    const int64_t blocks = most_tiles(p, 16 * MF) * p.n_blocks;
-    if (blocks * 64 * WAVES > INT32_MAX)
+    const int64_t blocks = most_tiles(p, 16) * p.n_blocks;
+    if (blocks * 64 * kWaves > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    k_mat_few<MF, NF, WAVES, U, SWIGLU, OUT><<<(unsigned)blocks, 64 * WAVES, 0, stream>>>(p);
+    k_mat_few<NF, kWaves, U, SWIGLU, OUT><<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p);
     return launched();
 }
 
-// Few tiles leave most of the GPU idle and their sum in one workgroup: there the wavefronts of a workgroup
-// share it, and 16 or 32 channels make a workgroup.
+// Experts with no more rows than a matrix instruction takes, and few tiles: the wavefronts of a workgroup
+// share the sum, and 16 or 32 channels make a workgroup.
 constexpr int64_t kFewTiles = 128;
 
+bool few(int32_t R, int32_t E, int64_t n_w)
+{
+    const int64_t experts = E < R ? E : R;
+    const int64_t tiles = E == 1 ? div_up(R, 32) : R / 32 + experts;
+    return div_up(R, experts) <= 16 && tiles * div_up(n_w, 128) < kFewTiles;
+}
+
 template <bool SWIGLU, typename OUT>
-moe_status_t launch_forward(const MatArgs& p, hipStream_t stream)
+moe_status_t launch_forward(const MatArgs& p, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const int64_t n_w = SWIGLU ? 2 * (int64_t)p.N : p.N;
-    if (most_tiles(p, 32) * div_up(n_w, 128) < kFewTiles) {
-        if (div_up(p.R, p.E < p.R ? p.E : p.R) > 16)
-            return launch_few<2, 2, 8, 4, SWIGLU, OUT>(p, stream);
+    if (few(p.R, p.E, n_w)) {
         if (SWIGLU || most_tiles(p, 16) * div_up(n_w, 16) > 512)
-            return launch_few<1, 2, 8, 4, SWIGLU, OUT>(p, stream);
-        return launch_few<1, SWIGLU ? 2 : 1, 8, SWIGLU ? 4 : 2, SWIGLU, OUT>(p, stream);
+            return launch_few<2, 4, SWIGLU, OUT>(p, stream);
+        return launch_few<SWIGLU ? 2 : 1, SWIGLU ? 4 : 2, SWIGLU, OUT>(p, stream);
     }
-    const int shape = choose<kForward>(p.R, p.E, 0, n_w, p.D).shape;
+    const Plan plan = choose<kForward>(p.R, p.E, 0, n_w, p.D);
+    if (plan.splits > 1) {
+        if (!workspace || workspace_bytes < (size_t)plan.part_bytes)
+            return MOE_ERR_WORKSPACE;
+        MatArgs q = p, j = p;
+        q.splits = j.splits = plan.splits;
+        q.N = (int32_t)n_w;
+        q.out = workspace;
+        q.act = MOE_MAT_NONE;
+        q.bias = nullptr;
+        q.extra = nullptr;
+        q.pre = nullptr;
+        const moe_status_t st = launch_shape<kForward, false, false, float>(plan.shape, q, stream);
+        if (st != MOE_OK)
+            return st;
+        const int64_t need = div_up((int64_t)p.R * div_up(p.N, 4), 256), most = 8192;
+        k_join_forward<SWIGLU, OUT><<<(unsigned)(need < most ? need : most), 256, 0, stream>>>(
+            j, static_cast<const float*>(workspace));
+        return launched();
+    }
     if (p.pre || p.extra || (!SWIGLU && p.act != MOE_MAT_NONE))
-        return launch_shape<kForward, SWIGLU, true, OUT>(shape, p, stream);
-    return launch_shape<kForward, SWIGLU, false, OUT>(shape, p, stream);
+        return launch_shape<kForward, SWIGLU, true, OUT>(plan.shape, p, stream);
+    return launch_shape<kForward, SWIGLU, false, OUT>(plan.shape, p, stream);
 }
 
 }  // namespace
 
 extern "C" {
 
+size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K)
+{
+    if (R < 1 || E < 1 || channels < 1 || K < 1 || few(R, E, channels))
+        return 0;
+    return (size_t)choose<kForward>(R, E, 0, channels, K).part_bytes;
+}
+
 moe_status_t moe_expert_matmul(const void* a, int32_t a_rows, const int32_t* row_token,
                                const void* w, const float* bias, const int32_t* expert_offsets,
                                int32_t R, int32_t E, int32_t N, int32_t K, moe_mat_act_t act,
                                const void* residual, void* pre, void* out, moe_dtype_t out_dtype,
-                               hipStream_t stream)
+                               void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const int64_t n_w = act == MOE_MAT_SWIGLU ? 2 * (int64_t)N : N;
     const moe_status_t st = check_sizes(a_rows, row_token, expert_offsets, R, E, N, n_w, K, act);
@@ -197,7 +260,7 @@ moe_status_t moe_expert_matmul(const void* a, int32_t a_rows, const int32_t* row
     const int each = out_dtype == MOE_F32 ? 4 : 2;
     if (!aligned_to((const char*)a, 16) || !aligned_to((const char*)w, 16) || !aligned_to(bias, 4) ||
         !aligned_to((const char*)out, each) || !aligned_to((const char*)residual, each) ||
-        !aligned_to((const char*)pre, 2))
+        !aligned_to((const char*)pre, 2) || !aligned_to((const char*)workspace, 16))
         return MOE_ERR_UNSUPPORTED;
     if (R == 0)
         return MOE_OK;
@@ -210,10 +273,10 @@ moe_status_t moe_expert_matmul(const void* a, int32_t a_rows, const int32_t* row
     p.D = K;
     p.act = act;
     if (act == MOE_MAT_SWIGLU)
-        return out_dtype == MOE_BF16 ? launch_forward<true, __bf16>(p, stream)
-                                     : launch_forward<true, float>(p, stream);
-    return out_dtype == MOE_BF16 ? launch_forward<false, __bf16>(p, stream)
-                                 : launch_forward<false, float>(p, stream);
+        return out_dtype == MOE_BF16 ? launch_forward<true, __bf16>(p, workspace, workspace_bytes, stream)
+                                     : launch_forward<true, float>(p, workspace, workspace_bytes, stream);
+    return out_dtype == MOE_BF16 ? launch_forward<false, __bf16>(p, workspace, workspace_bytes, stream)
+                                 : launch_forward<false, float>(p, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -131,12 +131,17 @@ typedef enum {
  * expert's weights and, with row_token, all of
  * `a` below 4 GiB (else MOE_ERR_UNSUPPORTED); R <= a_rows without row_token (else MOE_ERR_INVALID).
  * R = 0 enqueues nothing.
+ *   workspace: moe_expert_matmul_workspace_bytes(R, E, channels of w, K) bytes, 16-byte aligned, any
+ *   contents, NULL where that is 0; calls that may run at the same time must not share one. Few tiles
+ *   with long sums (the gate of a few thousand tokens) are made in parts, joined in a fixed order.
  */
+size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K);
+
 moe_status_t moe_expert_matmul(const void* a, int32_t a_rows, const int32_t* row_token,
                                const void* w, const float* bias, const int32_t* expert_offsets,
                                int32_t R, int32_t E, int32_t N, int32_t K, moe_mat_act_t act,
                                const void* residual, void* pre, void* out, moe_dtype_t out_dtype,
-                               hipStream_t stream);
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Gradients of y[r, n] = sum_i a[s(r), i] * w[e, n, i] + bias[e, n] from dy [R, N] bf16:

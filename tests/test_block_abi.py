@@ -25,6 +25,7 @@ def test_every_declared_function_is_exported_and_bound():
     names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
     assert names == sorted(["moe_route_scored", "moe_route_scored_grad", "moe_bias_update",
                             "moe_combine_grad", "moe_expert_matmul", "moe_expert_matmul_grad",
+                            "moe_expert_matmul_workspace_bytes",
                             "moe_matmul_grad_workspace_bytes"])
     for n in names:
         assert hasattr(moe.load(), n) and callable(getattr(pkg, n)), n
@@ -107,12 +108,12 @@ def test_combine_grad_refusals():
 def test_expert_matmul_refusals():
     f = moe.load().moe_expert_matmul
     ok = dict(a=A16, A=8, rt=A16, w=A16b, b=None, off=A16, R=8, E=4, N=32, K=64, act=0, res=None,
-              pre=None, out=A16, od=BF16)
+              pre=None, out=A16, od=BF16, ws=None, wsb=0)
 
     def call(**kw):
         a = dict(ok, **kw)
         return f(a["a"], a["A"], a["rt"], a["w"], a["b"], a["off"], a["R"], a["E"], a["N"], a["K"],
-                 a["act"], a["res"], a["pre"], a["out"], a["od"], S0)
+                 a["act"], a["res"], a["pre"], a["out"], a["od"], a["ws"], a["wsb"], S0)
 
     for bad in (dict(R=-1), dict(A=-1), dict(E=0), dict(N=0), dict(K=0), dict(act=5), dict(act=-1),
                 dict(off=None), dict(rt=None, R=9), dict(A=0), dict(a=None), dict(w=None),
@@ -121,9 +122,15 @@ def test_expert_matmul_refusals():
     for bad in (dict(od=FP8), dict(K=68), dict(E=1025), dict(N=2 ** 21, K=1024),
                 dict(N=2 ** 20, K=1024, act=1), dict(A=2 ** 21, K=1024), dict(K=2 ** 22 + 8, N=1),
                 dict(N=2 ** 22 + 8, K=8), dict(a=MIS), dict(w=MIS), dict(b=ODD), dict(out=ODD, od=F32), dict(out=ODD),
-                dict(pre=ODD), dict(res=ODD)):
+                dict(pre=ODD), dict(res=ODD), dict(ws=MIS, wsb=1 << 30)):
         assert call(**bad) == UNS, bad
     assert call(R=0) == OK and call(R=0, a=None, w=None, out=None) == OK
+    sizes = dict(R=64, A=64, E=1, N=384, K=7168)
+    need = moe.moe_expert_matmul_workspace_bytes(64, 1, 384, 7168)
+    assert need > 0 and call(**sizes) == WSP and call(**sizes, ws=A16, wsb=need - 1) == WSP
+    assert moe.moe_expert_matmul_workspace_bytes(8, 4, 32, 64) == 0
+    for bad in ((-1, 4, 32, 64), (8, 0, 32, 64), (8, 4, 0, 64), (8, 4, 32, 0)):
+        assert moe.moe_expert_matmul_workspace_bytes(*bad) == 0
 
 
 def test_expert_matmul_grad_refusals():
@@ -180,6 +187,8 @@ def test_binding_refuses_sizes_beyond_int32():
     for sizes in ((over, 1, 1, 1), (1, over, 1, 1), (1, 1, over, 1), (1, 1, 1, over)):
         with pytest.raises(ValueError, match="2147483647"):
             moe.moe_matmul_grad_workspace_bytes(*sizes)
+        with pytest.raises(ValueError, match="2147483647"):
+            moe.moe_expert_matmul_workspace_bytes(*sizes)
 
 
 def differences(f, x, h=1e-5):

@@ -384,6 +384,68 @@ def test_expert_matmul_masked_places():
         assert not torch.isfinite(rest[hit]).any() and torch.equal(rest[~hit], same[~hit])
 
 
+# Few tiles with long sums, which are made in parts and joined.
+FORWARD_PART_SHAPES = [
+    (64, 1, 384, 7168, "even"), (24, 1, 64, 4096, "even"), (70, 1, 10, 8200, "even"), (17, 1, 264, 1096, "even"),
+    (130, 2, 33, 4104, "uneven"), (300, 8, 66, 2048, "uneven"), (200, 5, 136, 3000, "one"),
+    (333, 3, 130, 1544, "uneven"), (4096, 1, 60, 2048, "even"),
+]
+
+
+@pytest.mark.parametrize("act,dtype", [("none", F32), ("swiglu", BF16), ("swiglu", F32), ("gelu", BF16)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,E,N,K,kind", FORWARD_PART_SHAPES)
+def test_expert_matmul_in_parts(T, E, N, K, kind, gather, act, dtype):
+    _announce(f"bf16 matmul in parts T={T} E={E} N={N} K={K} {kind} gather={gather} {act} {dtype}")
+    n_w = 2 * N if act == "swiglu" else N
+    assert moe.moe_expert_matmul_workspace_bytes(T, E, n_w, K) >= 8 * T * n_w
+    check_product(T, 1, E, N, K, gather, kind, act, dtype, gather, act != "none", act != "gelu", seed=T + N + K)
+
+
+def test_expert_matmul_in_parts_rows_left_alone():
+    """Rows behind the last expert's, rows whose row_token is out of range, and NaN in a workspace whose
+    contents nobody gave."""
+    for T, E, N, K, act in ((300, 8, 66, 2048, "none"), (200, 5, 136, 3000, "swiglu"), (130, 2, 33, 4104, "relu")):
+        _announce(f"bf16 matmul in parts, rows left alone T={T} E={E} N={N} K={K} {act}")
+
+        def spoil(rt):
+            rt[[0, T // 4, T // 2, T - 1]] = [-1, T, 2 ** 31 - 1, -2 ** 31]
+            return rt
+
+        check_product(T, 1, E, N, K, True, "uneven", act, BF16, True, False, True,
+                      offsets=lambda o: np.minimum(o, T - T // 3).astype(np.int32), rt=spoil, seed=N)
+        rng, R, o, a, rt = make(T, 1, E, N, K, True, "uneven")
+        n_w = 2 * N if act == "swiglu" else N
+        w = bf16(rng, E, n_w, K)
+        ws = moe.alloc_expert_matmul_workspace(R, E, n_w, K)
+        ws.fill_(255)
+        assert torch.equal(run_product(a, w, o, rt, act=act, workspace=ws), run_product(a, w, o, rt, act=act))
+        with pytest.raises(moe.MoeError):
+            run_product(a, w, o, rt, act=act, workspace=ws[:-16])
+    with pytest.raises(ValueError, match="workspace"):
+        moe.moe_expert_matmul(a.cuda(), w.cuda(), dev(o), row_token=dev(rt), act=act,
+                              workspace=torch.empty(1 << 24, dtype=torch.uint8))
+
+
+def test_expert_matmul_in_parts_same_bits_captured():
+    """Two runs have the same bits, and a captured one in its own workspace too, replayed between other
+    work that uses memory."""
+    _announce("bf16 matmul in parts, captured")
+    rng, R, o, a, rt = make(200, 1, 1, 384, 7168, False, "even")
+    a, w, o = a.cuda(), bf16(rng, 1, 384, 7168).cuda(), dev(o)
+    want = moe.moe_expert_matmul(a, w, o, out_dtype=F32)
+    ws, out = moe.alloc_expert_matmul_workspace(200, 1, 384, 7168), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_expert_matmul(a, w, o, out=out, out_dtype=F32, workspace=ws)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        other = moe.moe_expert_matmul(a, w, o, out_dtype=F32)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(other, want)
+
+
 # ---------------------------------------------------------------------- gradients of products --
 def check_grad(T, k, E, N, K, gather, kind, act, da_dtype, dw_dtype, plain=False, offsets=None, rt=None,
                seed=0):
