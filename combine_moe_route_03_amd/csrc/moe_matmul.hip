@@ -6,14 +6,18 @@
 namespace {
 
 // ---- few rows ----
-// Bound by reading the weights, each once: a workgroup takes up to 16 rows of one expert and 16 NF
-// channels; its wavefronts share the sum out by 128-byte pieces, read weights and rows straight into
-// operands, and add their fp32 sums up through LDS, in wavefront order. v_mfma_f32_16x16x32_bf16 with
-// the weights as the left operand: lane l gives channel l % 16 and 16 bytes of the sum at 16 (l / 16),
-// and gets row l % 16 with channels 4 (l / 16) + i.
-template <int NF, int WAVES, int U, bool SWIGLU, typename OUT>
+// Bound by reading the weights, each once: a workgroup takes up to 16 rows of one expert and 16 channels
+// (with SwiGLU, gate and up of 16); its eight wavefronts share the sum out by 128-byte pieces, read
+// weights and rows straight into operands, and add their fp32 sums up through LDS, in wavefront order:
+// no wait in the loop but for the operands, and eight times the loads on their way that a tile with all
+// of the sum to itself has. 8 rows of 8 experts by 2 x 1024 channels of 2048 14.9 us (floor at 6.5 TB/s
+// 10.3), one token by 384 of 7168 9.7. v_mfma_f32_16x16x32_bf16 with the weights as the left operand: lane
+// l gives channel l % 16 and 16 bytes of the sum at 16 (l / 16), and gets row l % 16 with channels
+// 4 (l / 16) + i.
+template <int WAVES, int U, bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
 {
+    constexpr int NF = SWIGLU ? 2 : 1;                        // fragments
     __shared__ f32x4 s_acc[WAVES][NF][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t nb = blockIdx.x % p.n_blocks;
@@ -24,27 +28,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
     const int32_t n_w = SWIGLU ? 2 * p.N : p.N;               // channels of w
     const __bf16* we = p.cols + (int64_t)tile.e * n_w * p.D;
 
-    // channels: fragment f covers 16 from n0 + 16 f; with SwiGLU even fragments hold the gate and
-    // the odd ones the same channels' up
-    const int32_t n0 = nb * (SWIGLU ? 8 * NF : 16 * NF);
+    const int32_t n0 = nb * 16;                               // SwiGLU: the first fragment's is the gate,
     const __bf16* wp[NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-        int32_t n = SWIGLU ? n0 + 16 * (f / 2) + r16 : n0 + 16 * f + r16;
-        n = min(n, p.N - 1) + (SWIGLU && (f & 1) ? p.N : 0);
+        const int32_t n = min(n0 + r16, p.N - 1) + f * p.N;   // the other's the same channels' up
         wp[f] = we + (int64_t)n * p.D;
     }
     const int32_t row = tile.row0 + min(r16, tile.rows - 1);
     const int32_t src = p.row_token ? p.row_token[row] : row;
     const bool there = (uint32_t)src < (uint32_t)p.a_rows;    // else its results are not stored
     const __bf16* ap = p.rows + (int64_t)(there ? src : 0) * p.D;
-    // the fragment (with SwiGLU the pair) that this wavefront will join and store
-    constexpr int kStep = SWIGLU ? 2 : 1;
-    static_assert(NF <= WAVES * kStep, "one for a wavefront");
-    const int mine = wave * kStep;
-    const int32_t n = n0 + (SWIGLU ? 8 : 16) * mine + 4 * kq;
+    // the first wavefront joins the sums and stores
+    const int32_t n = n0 + 4 * kq;
     const int32_t left = p.N - n;
-    const bool stores = mine < NF && r16 < tile.rows && there && left > 0;
+    const bool stores = wave == 0 && r16 < tile.rows && there && left > 0;
     const bool vec = p.N % 4 == 0;
     f32x4 b0 = {0.0f, 0.0f, 0.0f, 0.0f}, b1 = b0, res = b0;
     if (stores && p.bias) {
@@ -88,15 +86,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
     __syncthreads();
     if (!stores)
         return;
-    f32x4 sum[2];
+    f32x4 sum[NF];
 #pragma unroll
-    for (int g = 0; g < kStep; ++g) {
-        sum[g] = s_acc[0][mine + g][lane];
+    for (int f = 0; f < NF; ++f) {
+        sum[f] = s_acc[0][f][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w)
-            sum[g] += s_acc[w][mine + g][lane];
+            sum[f] += s_acc[w][f][lane];
     }
-    f32x4 y = sum[0] + b0, up = sum[kStep - 1] + b1;
+    f32x4 y = sum[0] + b0, up = sum[NF - 1] + b1;
     if (p.pre) {
         __bf16* q = p.pre + (int64_t)row * n_w + n;
         store4(q, round4<__bf16>(y), left);
@@ -117,7 +115,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_mat_few(MatArgs p)
 
 // ---- sums in parts ----
 // Adds up `splits` parts [R, n_w] in order and does what else there is to a result: four columns of a row
-// a thread.
+// a thread. Parts stay in fp32, so that out is rounded once here too. Bound by their bytes and a launch: 64
+// rows by 384 channels of 7168 in 16 parts 13.0 us with it (4.5 of them), 32.8 without parts (16 loads
+// one behind the other: 17.0); 4096 rows in 4 parts 48 and 72.
 template <bool SWIGLU, typename OUT>
 __global__ __launch_bounds__(256) void k_join_forward(MatArgs p, const float* __restrict__ parts)
 {
@@ -175,21 +175,25 @@ __global__ __launch_bounds__(256) void k_join_forward(MatArgs p, const float* __
     }
 }
 
-template <int NF, int U, bool SWIGLU, typename OUT>
+template <bool SWIGLU, typename OUT>
 moe_status_t launch_few(MatArgs p, hipStream_t stream)
 {
     constexpr int kWaves = 8;
-    p.n_blocks = (int32_t)div_up(p.N, SWIGLU ? 8 * NF : 16 * NF);
+    p.n_blocks = (int32_t)div_up(p.N, 16);
     const int64_t blocks = most_tiles(p, 16) * p.n_blocks;
     if (blocks * 64 * kWaves > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    k_mat_few<NF, kWaves, U, SWIGLU, OUT><<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p);
+    k_mat_few<kWaves, SWIGLU ? 4 : 2, SWIGLU, OUT><<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p);
     return launched();
 }
 
-// Experts with no more rows than a matrix instruction takes, and few tiles: the wavefronts of a workgroup
-// share the sum, and 16 or 32 channels make a workgroup.
-constexpr int64_t kFewTiles = 128;
+// Experts with no more rows than a matrix instruction takes, and tiles (of 32 rows by 128 channels) for
+// less than a workgroup a CU: k_mat_few; else the tiles of moe_mat_tile.h, here and there (us): 16 rows by
+// 2048 channels of 2048 (16 tiles) 8.4 and 11.6, by 16384 of 1024 (128) 10.0 and 14.2, 8 rows of 64 experts
+// by 2 x 1408 of 2048 (176) 19.1 and 21.5, 16 rows by 32768 of 1024 (256) 16.9 and 14.2, one token by 32768
+// of 2048 (256) 28 and 26, 32 rows of 128 experts by 2 x 1024 of 2048 (528) 43 and 34. 32 channels a
+// workgroup: 8.7, 13.4 and 24 us for the second, third and fifth.
+constexpr int64_t kFewTiles = 256;
 
 bool few(int32_t R, int32_t E, int64_t n_w)
 {
@@ -203,9 +207,7 @@ moe_status_t launch_forward(const MatArgs& p, void* workspace, size_t workspace_
 {
     const int64_t n_w = SWIGLU ? 2 * (int64_t)p.N : p.N;
     if (few(p.R, p.E, n_w)) {
-        if (SWIGLU || most_tiles(p, 16) * div_up(n_w, 16) > 512)
-            return launch_few<2, 4, SWIGLU, OUT>(p, stream);
-        return launch_few<SWIGLU ? 2 : 1, SWIGLU ? 4 : 2, SWIGLU, OUT>(p, stream);
+        return launch_few<SWIGLU, OUT>(p, stream);
     }
     const Plan plan = choose<kForward>(p.R, p.E, 0, n_w, p.D);
     if (plan.splits > 1) {
@@ -238,7 +240,8 @@ extern "C" {
 
 size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K)
 {
-    if (R < 1 || E < 1 || channels < 1 || K < 1 || few(R, E, channels))
+    if (R < 1 || E < 1 || channels < 1 || K < 1 || E > MOE_MAX_EXPERTS || channels > MOE_MAT_MAX_SIZE ||
+        K > MOE_MAT_MAX_SIZE || few(R, E, channels))
         return 0;
     return (size_t)choose<kForward>(R, E, 0, channels, K).part_bytes;
 }

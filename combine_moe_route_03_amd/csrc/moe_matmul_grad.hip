@@ -170,7 +170,8 @@ extern "C" {
 
 size_t moe_matmul_grad_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K)
 {
-    if (R < 0 || E < 1 || N < 1 || K < 1)
+    if (R < 0 || E < 1 || N < 1 || K < 1 || E > MOE_MAX_EXPERTS || N > MOE_MAT_MAX_SIZE ||
+        K > MOE_MAT_MAX_SIZE)
         return 0;
     int64_t bytes = 256;
     if (R > 0) {
@@ -198,7 +199,8 @@ moe_status_t moe_expert_matmul_grad(const void* dy, const void* a, int32_t a_row
         return MOE_ERR_INVALID;
     if (N % 8 != 0 || (da && da_dtype != MOE_F32 && da_dtype != MOE_BF16) ||
         (dw && dw_dtype != MOE_F32 && dw_dtype != MOE_BF16) ||
-        (act == MOE_MAT_SWIGLU && K > MOE_MAT_MAX_SIZE / 2))
+        (act == MOE_MAT_SWIGLU && K > MOE_MAT_MAX_SIZE / 2) ||
+        (dbias && E * div_up(N, 128) > INT32_MAX / 256))      // one workgroup of 256 for each
         return MOE_ERR_UNSUPPORTED;
     if (R > 0 && (!dy || (da && (!w || (act != MOE_MAT_NONE && !pre))) || (dw && !a)))
         return MOE_ERR_INVALID;

@@ -128,11 +128,11 @@ typedef enum {
  * a row whose row_token lies outside [0, a_rows). Offsets outside [0, R] or falling break the
  * preconditions and leave the rows of the outputs unspecified.
  * Requires K % 8 == 0, K and the channels of w <= MOE_MAT_MAX_SIZE, E <= MOE_MAX_EXPERTS, and one
- * expert's weights and, with row_token, all of
- * `a` below 4 GiB (else MOE_ERR_UNSUPPORTED); R <= a_rows without row_token (else MOE_ERR_INVALID).
+ * expert's weights and, with row_token, all of `a` below 4 GiB (else MOE_ERR_UNSUPPORTED); R <= a_rows
+ * without row_token (else MOE_ERR_INVALID).
  * R = 0 enqueues nothing.
  *   workspace: moe_expert_matmul_workspace_bytes(R, E, channels of w, K) bytes, 16-byte aligned, any
- *   contents, NULL where that is 0; calls that may run at the same time must not share one. Few tiles
+ *   contents, NULL where that is 0 (sizes that the product refuses have 0 too); calls that may run at the same time must not share one. Few tiles
  *   with long sums (the gate of a few thousand tokens) are made in parts, joined in a fixed order.
  */
 size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K);

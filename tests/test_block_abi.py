@@ -129,7 +129,8 @@ def test_expert_matmul_refusals():
     need = moe.moe_expert_matmul_workspace_bytes(64, 1, 384, 7168)
     assert need > 0 and call(**sizes) == WSP and call(**sizes, ws=A16, wsb=need - 1) == WSP
     assert moe.moe_expert_matmul_workspace_bytes(8, 4, 32, 64) == 0
-    for bad in ((-1, 4, 32, 64), (8, 0, 32, 64), (8, 4, 0, 64), (8, 4, 32, 0)):
+    for bad in ((-1, 4, 32, 64), (8, 0, 32, 64), (8, 4, 0, 64), (8, 4, 32, 0), (8, 2 ** 31 - 1, 32, 64),
+                (2 ** 31 - 1, 4, 2 ** 31 - 1, 64), (8, 4, 32, 2 ** 31 - 1)):
         assert moe.moe_expert_matmul_workspace_bytes(*bad) == 0
 
 
@@ -154,8 +155,10 @@ def test_expert_matmul_grad_refusals():
                 dict(da=MIS), dict(dw=MIS), dict(ws=MIS)):
         assert call(**dict(bad, wsb=1 << 62)) == UNS, bad
     assert need > 0 and call(ws=None) == WSP and call(wsb=need - 1) == WSP
-    for bad in ((-1, 4, 32, 64), (8, 0, 32, 64), (8, 4, 0, 64), (8, 4, 32, 0)):
+    for bad in ((-1, 4, 32, 64), (8, 0, 32, 64), (8, 4, 0, 64), (8, 4, 32, 0), (8, 2 ** 31 - 1, 32, 64),
+                (2 ** 31 - 1, 4, 2 ** 31 - 1, 64), (8, 4, 32, 2 ** 31 - 1)):
         assert moe.moe_matmul_grad_workspace_bytes(*bad) == 0
+    assert call(E=1024, N=2 ** 22, K=8, da=None, dw=None, db=A16, wsb=1 << 62) == UNS
 
 
 def test_binding_refuses_tensors_that_do_not_fit():
