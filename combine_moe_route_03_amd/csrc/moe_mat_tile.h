@@ -189,12 +189,13 @@ __device__ __forceinline__ Work weights_at(const MatArgs& p, int32_t at)
 
 // Results of a wavefront's fragments, row lane % 32 and columns 8 i + 4 (lane / 32) + c of fragment
 // g in v[g][i], through a little LDS of its own and out as whole lines: 16-byte piece c of row r
-// lies in slot c ^ (r % 8). The stores go to the caches: where rows are no whole lines of 128 bytes, the L2
-// has to put together what different tiles write of a line (60 experts' weights of 264 x 5016 in fp32 74
-// us; past the caches 158, with whole lines 5% less or more).
+// lies in slot c ^ (r % 8). Rows of whole 64 bytes are stored past the caches (weights of 20 experts of 1000
+// x 2064 in fp32, with the other gradients, 98 us for 110, 32 experts of 4096 x 2048 1% either way); others
+// through them, where the L2 puts together what two tiles write of 64 bytes (weights of 60 experts of 264 x
+// 5016 in fp32 74 us for 158).
 template <int UNIT, typename OUT, int F>
 __device__ __forceinline__ void store_unit(int8_t* unit, const typename Four<OUT>::type (&v)[F][4],
-                                           OUT* base, __amdgpu_buffer_rsrc_t buffer, bool wide,
+                                           OUT* base, __amdgpu_buffer_rsrc_t buffer, bool wide, bool past,
                                            int32_t ld, int32_t n_end, int32_t tr, int32_t n1,
                                            uint32_t rows, int lane)
 {
@@ -230,8 +231,11 @@ __device__ __forceinline__ void store_unit(int8_t* unit, const typename Four<OUT
                 const int32_t n = n1 + c * (16 / (int)sizeof(OUT));
                 const uint32_t to = ((uint32_t)(tr0 + r) * (uint32_t)ld + (uint32_t)n) *
                                     (uint32_t)sizeof(OUT);
-                __builtin_amdgcn_raw_buffer_store_b128(out, buffer, (ok >> r & 1) && n < n_end ? to : kOut,
-                                                       0, 0);
+                const uint32_t at = (ok >> r & 1) && n < n_end ? to : kOut;
+                if (past)
+                    store_buffer(out, buffer, at);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(out, buffer, at, 0, 0);
             }
         } else {                                              // a value a lane, side by side
             constexpr int kCols = F * 32;
@@ -276,7 +280,7 @@ template <typename OUT>
 struct Sink {
     OUT* base;
     int32_t ld;
-    bool wide;
+    bool wide, past;
     __amdgpu_buffer_rsrc_t buffer;
 
     __device__ __forceinline__ Sink(OUT* out, int64_t row0, int32_t rows, int32_t n, int32_t parts)
@@ -285,6 +289,7 @@ struct Sink {
         base = out + row0 * columns;
         ld = columns;
         wide = n % (16 / (int)sizeof(OUT)) == 0 && (uintptr_t)out % 16 == 0 && columns <= (1 << 20);
+        past = n * (int64_t)sizeof(OUT) % 64 == 0 && (uintptr_t)out % 64 == 0;
         buffer = __builtin_amdgcn_make_buffer_rsrc(
             base, 0, (int32_t)((uint32_t)rows * (uint32_t)columns * (uint32_t)sizeof(OUT)),
             0x00020000);
@@ -828,16 +833,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
                         v[g][i] = round4<OUT>(y);
                     }
                 if (MODE == kForward && FULL && p.pre) {
-                    store_unit<kUnit, __bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.ld, p.N,
+                    store_unit<kUnit, __bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.past, pre.ld, p.N,
                                                tr, n1, rows, lane);
                     if (SWIGLU)
-                        store_unit<kUnit, __bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide, pre.ld,
+                        store_unit<kUnit, __bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide, pre.past, pre.ld,
                                                    n_w, tr, p.N + n1, rows, lane);
                 }
-                store_unit<kUnit, OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.ld, p.N, tr, n1,
+                store_unit<kUnit, OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.past, out.ld, p.N, tr, n1,
                                         rows, lane);
                 if (MODE == kRowsBack && FULL && paired)
-                    store_unit<kUnit, OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.ld, 2 * p.N,
+                    store_unit<kUnit, OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.past, out.ld, 2 * p.N,
                                             tr, p.N + n1, rows, lane);
             }
         }
