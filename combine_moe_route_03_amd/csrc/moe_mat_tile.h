@@ -325,7 +325,24 @@ __device__ __forceinline__ bf16x8 read_across(const int8_t* p)
     return __builtin_bit_cast(bf16x8, v);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool SWIGLU, bool FULL,
+// A tile of BM rows by BN columns by WM x WN wavefronts, each of BM / WM by BN / WN of it: the operands'
+// roles are exchanged in the instruction (columns left, rows right), so that a lane's sums are four columns
+// side by side of one row. A step is 64 terms of the sum: a stage of 128 bytes a line, filled by loads that
+// go straight to LDS, STAGES of them around. Operands along the sum: 16-byte piece c of line r lies in slot c
+// ^ (r / 2 % 8), which keeps the reads of 16 bytes off each other's banks (no conflicts counted; with r % 8
+// half of the LDS cycles were conflicts, in the same time). The four quarters of a step are read one
+// quarter ahead of their products, and the loads of a stage are spread out over the two quarters behind
+// its barrier (2% less time than all at once). Loads out of range write zeros, so the ends of sums, rows
+// that take no part and channels beyond the last cost no instructions. Sums stay in fp32 from the first
+// product to the epilogue; pre, out and da are rounded to their type once, at the end.
+// Bound by LDS and the matrix cores together: a 256 x 256 step takes 1.71 us, its products alone 0.86 at
+// 2.5 PFLOP/s. 8192 x 8192 x 8192 in forward form 926 us when taken apart (860 to
+// 890 since), without the loads 770, without the LDS reads 784, without the products 516: each takes over
+// half of the time and they overlap as far as two stages of 64 KB allow (a third does not fit). The
+// gradients of 8192^3: rows 880, weights 910 to 940 (a library product 779).
+// FULL: with pre, a residual, or an activation other than SwiGLU (rows: with an activation's
+// gradient), whose registers the other calls do not have to give up.
+template <int MODE, int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, bool FULL,
           typename OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
 {
@@ -610,8 +627,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
             av[set][m] = read_a(m, q);
     };
     // Multiplies operand set `cur` while quarter q goes into the other set. Fragments of rows that
-    // the tile does not have are left out. PIN: the reads stay spread out among the products. HALF: so
-    // are the loads of that half of a stage.
+    // the tile does not have are left out. Reads stay spread out among the products, and so are the
+    // loads of half a stage, if any.
     int32_t frags = MF;
     const auto multiply = [&](int cur, int q, auto which) {
         constexpr int kHalf = decltype(which)::value;
@@ -626,22 +643,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
 #pragma unroll
                     for (int n = place * kLoads / kPlaces; n < (place + 1) * kLoads / kPlaces; ++n)
                         load(n);
-                    if (PIN)
-                        __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 if (!live)
                     continue;
                 const int f = m & 1 ? NF - 1 - i : i;
                 acc[m][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[cur][f], av[cur][m],
                                                                     acc[m][f], 0, 0, 0);
-                if (PIN)
-                    __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
                 if (q >= 0 && i == 0)
                     av[1 - cur][m] = read_a(m, q);
                 if (q >= 0 && m == 0)
                     wv[1 - cur][i] = read_w(i, q);
-                if (PIN)
-                    __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
@@ -752,8 +766,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
         }
         at = next;
 
-        // Results, while the next tile's first stages are on their way. FULL: with more than a bias and
-        // SwiGLU. Stores of whole rows count the
+        // Results, while the next tile's first stages are on their way. Stores of whole rows count the
         // same for every wavefront, so that landed() can wait for the loads before them without them.
         const bool paired = MODE == kRowsBack && FULL && p.act == MOE_MAT_SWIGLU;
         const int64_t row0 = MODE == kWeightsBack ? ((int64_t)split * p.E + t.e) * p.M + t.row0
@@ -852,7 +865,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
 // WGS: persistent workgroups of a CU; kOnce: a workgroup for each tile, taken up as CUs come free.
 constexpr int kOnce = 1 << 20;
 
-template <int MODE, int BM, int BN, int WM, int WN, int STAGES, bool PIN, int WGS, bool SWIGLU,
+template <int MODE, int BM, int BN, int WM, int WN, int STAGES, int WGS, bool SWIGLU,
           bool FULL, typename OUT>
 inline moe_status_t launch_tile(MatArgs p, hipStream_t stream)
 {
@@ -869,7 +882,7 @@ inline moe_status_t launch_tile(MatArgs p, hipStream_t stream)
         most = INT32_MAX / kThreads / kXcds * kXcds;
     const int64_t blocks = tiles < most ? div_up(tiles, kXcds) * kXcds : most;
     p.max_tiles = (int32_t)rows;
-    const auto kernel = k_mat_tile<MODE, BM, BN, WM, WN, STAGES, PIN, SWIGLU, FULL, OUT>;
+    const auto kernel = k_mat_tile<MODE, BM, BN, WM, WN, STAGES, SWIGLU, FULL, OUT>;
     if (kStages > 49152) {                                    // once a device is enough
         static std::atomic<uint64_t> allowed{0};
         int dev = 0;
@@ -890,8 +903,10 @@ inline moe_status_t launch_tile(MatArgs p, hipStream_t stream)
 
 // The tile shapes, and what a step of 64 terms and a tile's beginning and end take (us, as measured with
 // every slot taken; `alone` with one workgroup a CU): 16384 channels by 4096 rows in one expert, K = 512
-// and 2048. Large tiles read less for each product (256 x 256: 1.25 PFLOP/s; 128 x 256: 1.1; 64 x 256:
-// 0.8), small ones waste less on experts with few rows and fill the GPU sooner.
+// and 2048. Large tiles read less for each product (256 x 256: 1.25 PFLOP/s; 128 x 256: 1.0; 64 x 256:
+// 0.85), small ones waste less on experts with few rows and fill the GPU sooner (98 rows of 60 experts,
+// rows' gradient by 5016 of 264: 67 us by 256 x 256, 38 by 64 x 256; 32768 rows of 32 experts by 2048 of
+// 4096: 525 and 804).
 struct TileCost {
     int32_t bm, bn, slots;
     float step, alone, tile;
@@ -910,7 +925,9 @@ constexpr TileCost kMatTiles[3][5] = {
 // How a product is made: its tile shape, and the parts of its sums. The least time by the
 // figures above: rounds of tiles over the slots, where an expert's last tile (weights: step) is half full
 // on average; the host knows the rows of all experts, not of each. Parts go through memory in fp32 and
-// are joined by a launch of its own, which only few tiles with long sums are worth.
+// are joined by a launch of its own, 4 us and their bytes, which only few tiles with long sums are worth
+// (4096 rows by 384 channels of 7168: 48 us in 4 parts, 72 in one); at most 16 parts and 256 MB of them, the
+// size of the Infinity Cache.
 struct Plan {
     int shape;
     int32_t splits;
@@ -958,17 +975,17 @@ inline moe_status_t launch_shape(int shape, const MatArgs& p, hipStream_t stream
 {
     if constexpr (MODE == kWeightsBack) {
         switch (shape) {
-        case 0: return launch_tile<MODE, 256, 256, 2, 4, 2, true, 1, SWIGLU, FULL, OUT>(p, stream);
-        case 1: return launch_tile<MODE, 128, 256, 2, 4, 2, true, 1, SWIGLU, FULL, OUT>(p, stream);
-        default: return launch_tile<MODE, 128, 128, 2, 2, 2, true, 2, SWIGLU, FULL, OUT>(p, stream);
+        case 0: return launch_tile<MODE, 256, 256, 2, 4, 2, 1, SWIGLU, FULL, OUT>(p, stream);
+        case 1: return launch_tile<MODE, 128, 256, 2, 4, 2, 1, SWIGLU, FULL, OUT>(p, stream);
+        default: return launch_tile<MODE, 128, 128, 2, 2, 2, 2, SWIGLU, FULL, OUT>(p, stream);
         }
     } else {
         switch (shape) {
-        case 0: return launch_tile<MODE, 256, 256, 2, 4, 2, true, 1, SWIGLU, FULL, OUT>(p, stream);
-        case 1: return launch_tile<MODE, 128, 256, 2, 4, 3, true, 1, SWIGLU, FULL, OUT>(p, stream);
-        case 2: return launch_tile<MODE, 128, 128, 2, 2, 2, true, 2, SWIGLU, FULL, OUT>(p, stream);
-        case 3: return launch_tile<MODE, 64, 256, 2, 4, 3, false, 1, SWIGLU, FULL, OUT>(p, stream);
-        default: return launch_tile<MODE, 32, 128, 1, 2, 3, false, kOnce, SWIGLU, FULL, OUT>(p, stream);
+        case 0: return launch_tile<MODE, 256, 256, 2, 4, 2, 1, SWIGLU, FULL, OUT>(p, stream);
+        case 1: return launch_tile<MODE, 128, 256, 2, 4, 3, 1, SWIGLU, FULL, OUT>(p, stream);
+        case 2: return launch_tile<MODE, 128, 128, 2, 2, 2, 2, SWIGLU, FULL, OUT>(p, stream);
+        case 3: return launch_tile<MODE, 64, 256, 2, 4, 3, 1, SWIGLU, FULL, OUT>(p, stream);
+        default: return launch_tile<MODE, 32, 128, 1, 2, 3, kOnce, SWIGLU, FULL, OUT>(p, stream);
         }
     }
 }

@@ -9,7 +9,8 @@ namespace {
 
 // ---- sums in parts ----
 // Adds up `splits` parts in order; four columns a thread. Rows of a: those of an expert, with the
-// activation's gradient; weights: all.
+// activation's gradient; weights: all. Parts and sums are fp32, results are rounded once. Bound by the
+// parts' bytes: 64 rows by 384 channels of 7168, rows' gradient 10 us with it, weights' 11.
 template <bool ROWS, typename OUT>
 __global__ __launch_bounds__(256) void k_join_parts(MatArgs p, const f32x4* __restrict__ parts,
                                                     int64_t total)
@@ -66,7 +67,10 @@ moe_status_t launch_join(const MatArgs& p, const void* parts, int64_t rows, hipS
 // ---- bias gradient ----
 // Column sums of dy over an expert's rows: 16 lanes hold 128 columns, 16 rows of a workgroup at a time and
 // eight of each lane on their way, each lane's rows in order and the 16 joined in order. The rows of an
-// expert are shared out over `splits` workgroups, whose sums are joined by a launch of its own.
+// expert are shared out over `splits` workgroups, whose sums are joined by a launch of its own. Bound by
+// latency where there are few rows, else by reading dy: 2331 rows of 20 experts by 1000 12.7 us with the
+// launch of the join (uneven experts without parts 18), 4096 rows by 384 12.6, 32768 rows of 256 experts by
+// 4096 44.7 (floor 41).
 __global__ __launch_bounds__(256) void k_bias_grad(MatArgs p, float* __restrict__ out)
 {
     constexpr int kFlight = 8;
@@ -121,19 +125,21 @@ __global__ __launch_bounds__(256) void k_join_bias(const float* __restrict__ par
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         float sum = parts[i];
+#pragma unroll 8
         for (int s = 1; s < splits; ++s)
             sum += parts[s * total + i];
         dbias[i] = sum;
     }
 }
 
-// Workgroups for the rows of an expert: four a CU in all, of 256 rows at least.
+// Workgroups for the rows of an expert: four a CU in all, of 16 rows at least where experts have the same
+// number, and 64 at most, whose sums the join adds up one by one (4096 rows by 384: 62 us with 256).
 int32_t bias_splits(int32_t R, int32_t E, int32_t N)
 {
     int64_t s = 1024 / ((int64_t)E * div_up(N, 128));
-    if (s > (int64_t)R / E / 256)
-        s = (int64_t)R / E / 256;
-    return s < 1 ? 1 : s > 256 ? 256 : (int32_t)s;
+    if (s > (int64_t)R / E / 16)
+        s = (int64_t)R / E / 16;
+    return s < 1 ? 1 : s > 64 ? 64 : (int32_t)s;
 }
 
 template <typename OUT>
