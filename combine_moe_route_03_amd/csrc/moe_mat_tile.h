@@ -846,17 +846,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_mat_tile(MatArgs p)
                         v[g][i] = round4<OUT>(y);
                     }
                 if (MODE == kForward && FULL && p.pre) {
-                    store_unit<kUnit, __bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.past, pre.ld, p.N,
-                                               tr, n1, rows, lane);
+                    store_unit<kUnit, __bf16, kUnitF>(unit, gate, pre.base, pre.buffer, pre.wide, pre.past,
+                                                      pre.ld, p.N, tr, n1, rows, lane);
                     if (SWIGLU)
-                        store_unit<kUnit, __bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide, pre.past, pre.ld,
-                                                   n_w, tr, p.N + n1, rows, lane);
+                        store_unit<kUnit, __bf16, kUnitF>(unit, up, pre.base, pre.buffer, pre.wide,
+                                                          pre.past, pre.ld, n_w, tr, p.N + n1, rows, lane);
                 }
-                store_unit<kUnit, OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.past, out.ld, p.N, tr, n1,
-                                        rows, lane);
+                store_unit<kUnit, OUT, kUnitF>(unit, v, out.base, out.buffer, out.wide, out.past, out.ld, p.N,
+                                               tr, n1, rows, lane);
                 if (MODE == kRowsBack && FULL && paired)
-                    store_unit<kUnit, OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.past, out.ld, 2 * p.N,
-                                            tr, p.N + n1, rows, lane);
+                    store_unit<kUnit, OUT, kUnitF>(unit, v2, out.base, out.buffer, out.wide, out.past, out.ld,
+                                                   2 * p.N, tr, p.N + n1, rows, lane);
             }
         }
     }

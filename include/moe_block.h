@@ -132,8 +132,9 @@ typedef enum {
  * without row_token (else MOE_ERR_INVALID).
  * R = 0 enqueues nothing.
  *   workspace: moe_expert_matmul_workspace_bytes(R, E, channels of w, K) bytes, 16-byte aligned, any
- *   contents, NULL where that is 0 (sizes that the product refuses have 0 too); calls that may run at the same time must not share one. Few tiles
- *   with long sums (the gate of a few thousand tokens) are made in parts, joined in a fixed order.
+ *   contents, NULL where that is 0 (it is also 0 for sizes that the product refuses); calls that may
+ *   run at the same time must not share one. Few tiles with long sums (the gate of a few thousand
+ *   tokens) are made in parts, joined in a fixed order.
  */
 size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K);
 
