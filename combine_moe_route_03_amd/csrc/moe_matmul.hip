@@ -192,7 +192,7 @@ moe_status_t launch_few(MatArgs p, hipStream_t stream)
 // 2048 channels of 2048 (16 tiles) 8.4 and 11.6, by 16384 of 1024 (128) 10.0 and 14.2, 8 rows of 64 experts
 // by 2 x 1408 of 2048 (176) 19.1 and 21.5, 16 rows by 32768 of 1024 (256) 16.9 and 14.2, one token by 32768
 // of 2048 (256) 28 and 26, 32 rows of 128 experts by 2 x 1024 of 2048 (528) 43 and 34. 32 channels a
-// workgroup: 8.7, 13.4 and 24 us for the second, third and fifth.
+// workgroup: 8.7, 13.4 and 24 us for the first, second and fourth.
 constexpr int64_t kFewTiles = 256;
 
 bool few(int32_t R, int32_t E, int64_t n_w)
