@@ -66,11 +66,11 @@ constexpr int kCus = 256;
 constexpr int kStepK = 128;              // bytes of a line in a stage: 64 terms of the sum
 
 // ------------------------------------------------------------------------------- epilogues --
-// GELU's tanh form is v sigmoid(t), t = 2 sqrt(2 / pi) (v + 0.044715 v^3).
+// GELU's tanh form is v / (1 + exp(-t)), t = 2 sqrt(2 / pi) (v + 0.044715 v^3).
 constexpr float kGelu = 1.59576912f, kCube = 0.044715f;
 
-// 1 / (1 + exp(-t)), with the rounding of t log2 e added back to first order, as in silu(). Below
-// -87 it stays at exp(-87), where everything made from it is below 1e-30.
+// 1 / (1 + exp(-t)), with the rounding of t log2 e added back to first order, as in logistic(). Below
+// -87 it stays at exp(-87); slope() makes of that what is below 1e-34.
 __device__ __forceinline__ float sigmoid(float t)
 {
     constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
@@ -88,7 +88,7 @@ __device__ __forceinline__ float activate(float v, int32_t act)
     if (act == MOE_MAT_SILU)
         return silu<true>(v);
     if (act == MOE_MAT_GELU)
-        return v * sigmoid(kGelu * __builtin_fmaf(kCube * v * v, v, v));
+        return logistic<true>(v, kGelu * __builtin_fmaf(kCube * v * v, v, v));
     return v;
 }
 

@@ -74,28 +74,34 @@ __device__ __forceinline__ Tile find_tile(const Args& p, int32_t index)
                 __builtin_amdgcn_readfirstlane(min(BM, n - left * BM)), 0};
 }
 
-// gate / (1 + exp(-gate)), with exp(x) = 2^(x log2 e): the product's rounding, |gate| 2^-24 of the
-// result, is added back to first order; v_exp_f32 and v_rcp_f32 are good to one ulp. FAR: any gate.
-// Above t = 96, where 1 is nothing next to exp, both work on its root and silu is
-// gate / sqrt(exp) / sqrt(exp): exp itself overflows from t = 128 (gate -88.7) and its reciprocal is
-// flushed from 126, but silu is a normal number down to gate -92. Beyond |t| = 192 the root goes
-// without its correction, which an infinite t would make infinite or NaN.
+// v / (1 + exp(-t)), with exp(x) = 2^(x log2 e): the product's rounding, |t| 2^-24 of the result, is
+// added back to first order; v_exp_f32 and v_rcp_f32 are good to one ulp. FAR: any t. Above
+// x = 96, where 1 is nothing next to exp, both work on its root and the result is v / sqrt(exp) /
+// sqrt(exp): exp itself overflows from x = 128 (t -88.7) and its reciprocal is flushed from 126, but
+// silu, where v is t, is a normal number down to -92. Beyond |x| = 192 the root goes without its
+// correction, which an infinite x would make infinite or NaN.
+template <bool FAR>
+__device__ __forceinline__ float logistic(float v, float t)
+{
+    constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
+    const float x = t * hi;
+    const float rest = (__builtin_fmaf(t, hi, -x) + t * lo) * 0.693147182f;
+    if (!FAR) {
+        const float e = __builtin_amdgcn_exp2f(x);
+        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest, e));
+    }
+    const bool far = x > 96.0f;
+    const float half = far ? 0.5f : 1.0f;
+    const float e = __builtin_amdgcn_exp2f(x * half);
+    const float s = __builtin_fabsf(x) > 192.0f ? e : __builtin_fmaf(e, rest * half, e);
+    const float r = __builtin_amdgcn_rcpf((far ? 0.0f : 1.0f) + s);
+    return v * r * (far ? r : 1.0f);
+}
+
 template <bool FAR>
 __device__ __forceinline__ float silu(float gate)
 {
-    constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
-    const float t = gate * hi;
-    const float rest = (__builtin_fmaf(gate, hi, -t) + gate * lo) * 0.693147182f;
-    if (!FAR) {
-        const float e = __builtin_amdgcn_exp2f(t);
-        return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest, e));
-    }
-    const bool far = t > 96.0f;
-    const float half = far ? 0.5f : 1.0f;
-    const float e = __builtin_amdgcn_exp2f(t * half);
-    const float s = __builtin_fabsf(t) > 192.0f ? e : __builtin_fmaf(e, rest * half, e);
-    const float r = __builtin_amdgcn_rcpf((far ? 0.0f : 1.0f) + s);
-    return gate * r * (far ? r : 1.0f);
+    return logistic<FAR>(gate, gate);
 }
 
 // silu(gate) * up of four channels. Gates up to 64 have the same bits by both forms, so a row's
