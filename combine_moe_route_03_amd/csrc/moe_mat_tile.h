@@ -70,15 +70,15 @@ constexpr int kStepK = 128;              // bytes of a line in a stage: 64 terms
 constexpr float kGelu = 1.59576912f, kCube = 0.044715f;
 
 // 1 / (1 + exp(-t)), with the rounding of t log2 e added back to first order, as in logistic(). Below
-// -87 it stays at exp(-87); slope() makes of that what is below 1e-34.
+// -87, where it leaves the normal numbers, it is 0.
 __device__ __forceinline__ float sigmoid(float t)
 {
     constexpr float hi = -1.44269502f, lo = -1.92596299e-8f;
-    t = fmaxf(t, -87.0f);
     const float x = t * hi;
     const float rest = (__builtin_fmaf(t, hi, -x) + t * lo) * 0.693147182f;
     const float e = __builtin_amdgcn_exp2f(x);
-    return __builtin_amdgcn_rcpf(1.0f + (t > 87.0f ? 0.0f : __builtin_fmaf(e, rest, e)));
+    const float r = __builtin_amdgcn_rcpf(1.0f + (t > 87.0f ? 0.0f : __builtin_fmaf(e, rest, e)));
+    return t < -87.0f ? 0.0f : r;
 }
 
 __device__ __forceinline__ float activate(float v, int32_t act)
@@ -93,7 +93,8 @@ __device__ __forceinline__ float activate(float v, int32_t act)
 }
 
 // The activation's slope at v: s (1 + v (1 - s)) of SiLU, s (1 + v (1 - s) t') of GELU. Both are 0
-// and 1 to fp32 from 100 on, where v is taken for its bound; a NaN stays one.
+// and 1 to fp32 from 100 on, where v is taken for its bound; a NaN stays one. Where s is taken for 0
+// the slope is below 4e-36.
 __device__ __forceinline__ float slope(float v, int32_t act)
 {
     if (act == MOE_MAT_RELU)

@@ -65,3 +65,59 @@ def test_activations_over_the_whole_range(R, E, N, K, act, dtype):
         # one rounding of nothing: the sum is a bf16 value
         g = f64(pre[:, 0])
         assert ((g == part) | (np.isnan(g) & np.isnan(part))).all()
+
+
+# rows, experts, terms of the sum (channels of dy), columns of da: tiles of several shapes, sums in parts
+SLOPE_WAYS = [(VALUES.size, 1, 16, 24), (VALUES.size, 4, 40, 136), (2000, 2, 264, 136), (4096, 1, 64, 1024),
+              (100, 1, 4096, 64)]
+
+
+def slope_of(v, act):
+    """(slope, bound of its fp32 error) of s (1 + x (1 - s)), s the logistic function of t, x = v t': s is good
+    to e = (24 + 8 |t|) u of itself, and 1 - s to e s + u."""
+    if act == "relu":
+        return (v > 0).astype(np.float64), np.zeros_like(v)
+    near = np.clip(v, -1e4, 1e4)                              # both slopes are 0 and 1 long before
+    gelu = act == "gelu"
+    t = np.sqrt(8 / np.pi) * (near + 0.044715 * near ** 3) if gelu else near
+    x = near * (np.sqrt(8 / np.pi) * (1 + 3 * 0.044715 * near * near) if gelu else 1.0)
+    with np.errstate(over="ignore"):
+        s, rest = 1.0 / (1.0 + np.exp(-t)), 1.0 / (1.0 + np.exp(t))
+    e = (24 + 8 * np.minimum(np.abs(t), 100)) * ref.U
+    ax = np.where(t < 100, np.abs(x), 0.0)                    # 1 - s is 0 beyond
+    d = s * (1 + x * rest)
+    return d, np.abs(d) * e + s * ax * (e * s + 3 * ref.U)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("R,E,N,K", SLOPE_WAYS)
+def test_activation_slopes_over_the_whole_range(R, E, N, K, act, dtype):
+    """Gradients that are exactly a value, small and large, times the slope at every value. Where the logistic
+    function is below exp(-87) a slope is at most (1 + |v t'|) exp(-87) < 2^-117 and may be 0; from -100 on it
+    is 0 in fp32, and so is whatever it is multiplied with. SwiGLU's up channels are moderate and large."""
+    _announce(f"slope of {act} over the range R={R} E={E} N={N} K={K} {dtype}")
+    for d, up in ((1.0, 2.0), (-2.0 ** 100, -3.0), (2.0, 2.0 ** 120)):
+        v = np.resize(VALUES, R)
+        off = np.linspace(0, R, E + 1).astype(np.int32)
+        dy = rows_of_one(np.full(R, d), R, N).cuda()
+        w = torch.ones((E, N, K), dtype=BF16, device="cuda")
+        pre = torch.from_numpy(v).bfloat16()[:, None].expand(R, K)
+        if act == "swiglu":
+            pre = torch.cat([pre, torch.full((R, K), up, dtype=BF16)], 1)
+        da, = moe.moe_expert_matmul_grad(dy, None, w, dev(off), want="da", act=act, pre=pre.contiguous().cuda(),
+                                         da_dtype=dtype)
+        slope, err = slope_of(v, act)
+        scale = d * up if act == "swiglu" else d
+        tol = np.abs(scale) * (err + 4 * ref.U * np.abs(slope) + (0.0 if act == "relu" else 2.0 ** -117))
+        tol = tol + np.abs(scale * slope) * ref.half(dtype == BF16) + FLUSHED
+        zero = v <= -100.0
+        for c in (0, K // 2, K - 1):
+            got = f64(da[:, c])
+            bad = np.where(zero, got != 0.0, ~(np.abs(got - scale * slope) <= tol))
+            assert not bad.any(), (d, c, v[bad][:4], got[bad][:4], (scale * slope)[bad][:4])
+            if act == "swiglu":                               # up: dh silu(gate)
+                with np.errstate(over="ignore", invalid="ignore"):
+                    want = d * ref.act(v, "silu")
+                close(f64(da[:, K + c]), want, (20 + 8 * np.minimum(np.abs(v), 100)) * ref.U + ref.half(dtype == BF16),
+                      FLUSHED * max(1.0, abs(d)), f"up, column {c}", v)
