@@ -354,11 +354,23 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs a)
     }
 }
 
+// A launch takes 2^31 threads: from 2^32 on the runtime takes the number of threads modulo 2^32, without an
+// error. 2^27 tokens of 16 lanes, 2^25 of 64.
 template <int G, int P>
-void launch_route(const RouteArgs& a, hipStream_t stream)
+void launch_route(RouteArgs a, hipStream_t stream)
 {
+    constexpr int32_t kTokens = (1 << 23) * (256 / G);
     const size_t lds = (size_t)(256 / G) * (a.E + 2 * a.groups + 1) * sizeof(double);
-    k_route_scored<G, P><<<(unsigned)div_up(a.T, 256 / G), 256, lds, stream>>>(a);
+    int32_t left = a.T;
+    for (; left > kTokens; left -= kTokens) {
+        a.T = kTokens;
+        k_route_scored<G, P><<<kTokens / (256 / G), 256, lds, stream>>>(a);
+        a.logits += (int64_t)kTokens * a.E;
+        a.idx += (int64_t)kTokens * a.k;
+        a.w += (int64_t)kTokens * a.k;
+    }
+    a.T = left;
+    k_route_scored<G, P><<<(unsigned)div_up(left, 256 / G), 256, lds, stream>>>(a);
 }
 
 // 16 lanes a token take two thirds of the instructions, or half, of a wavefront a token, which spreads few

@@ -159,3 +159,20 @@ def test_route_scored_long_ids_are_valid_whatever_the_logits(score):
         assert (1 + (of[:, 1:] != of[:, :-1]).sum(axis=1)).max() <= kept
         want = route(l[clean], None, k, score, groups, kept, 2, True, 1.0)[0]
         assert np.array_equal(idx[clean], want)
+
+
+@pytest.mark.parametrize("T,E,k", [(2 ** 28 + 5, 1, 1), (2 ** 26 + 5, 17, 17)])
+def test_route_scored_of_more_tokens_than_a_launch_takes(T, E, k):
+    """2^32 threads and more, by 16 lanes a token and by 64: tokens at the ends, and around every border where a
+    launch of 2^31 threads can end, have what they have alone."""
+    _announce(f"route_scored of {T} tokens, E={E} k={k}")
+    logits = torch.empty((T, E), device="cuda").normal_()
+    idx, w = moe.moe_route_scored(logits, k, score="sigmoid", renormalize=False)
+    lanes = 16 if k <= 16 else 64
+    for at in (0, 2 ** 31 // lanes, 2 ** 32 // lanes, T - 1):
+        rows = slice(max(0, at - 40), min(T, at + 40))
+        ti, tw = moe.moe_route_scored(logits[rows].contiguous(), k, score="sigmoid", renormalize=False)
+        assert torch.equal(idx[rows], ti) and torch.equal(w[rows], tw), at
+    assert int(idx.min()) == 0 and int(idx.max()) == E - 1
+    del logits, idx, w
+    torch.cuda.empty_cache()
