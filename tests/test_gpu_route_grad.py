@@ -66,3 +66,58 @@ def test_gradient_of_a_token_that_is_sure(T, E, k, score, renormalize):
     dw = (3 + rng.standard_normal((T, k))).astype(np.float32)
     got = moe.moe_route_scored_grad(dev(logits), dev(idx), dev(dw), score=score, renormalize=renormalize, scale=2.5)
     off(f64(got), *sharp_grad(logits, idx, dw, score, renormalize, 2.5), "dlogits")
+
+
+def plain_grad(x, idx, dw, add, score, renormalize, scale):
+    """(dlogits, tolerance) of many tokens, on the GPU in 64 bits; ids out of range take no part. The tolerance is
+    that of block_ref.scored_grad with the spread of normal logits, 2 * 6 at the most."""
+    T, E = x.shape
+    k = idx.shape[1]
+    ok = (idx >= 0) & (idx < E)
+    at, g = idx.clamp(0, E - 1).long(), torch.where(ok, dw.double(), 0.0)
+    s = torch.sigmoid(x.double()) if score == "sigmoid" else torch.softmax(x.double(), 1)
+    rel = (4 * (2 * 24 + 30) + k + 16) * ref.U
+    if score == "softmax" and not renormalize:
+        q = torch.zeros_like(s).scatter_add_(1, at, g)
+        d = scale * s * (q - (s * q).sum(1, keepdim=True))
+        size = s * (q.abs() + (s * q.abs()).sum(1, keepdim=True)) * (rel + E / 16 * ref.U)
+        mag = torch.zeros_like(s).scatter_add_(1, at, g.abs())
+        size = torch.maximum(size, s * (mag + (s * mag).sum(1, keepdim=True)) * (rel + E / 16 * ref.U))
+    else:
+        v = torch.where(ok, s.gather(1, at), 0.0)
+        slope = 1.0 if score == "softmax" else torch.sigmoid(-x.double().gather(1, at))
+        if renormalize:
+            total = v.sum(1, keepdim=True)
+            v = torch.where(total > 0, v / total, 0.0)
+            term = v * (g - (v * g).sum(1, keepdim=True)) * slope
+            size = v * (g.abs() + (v * g.abs()).sum(1, keepdim=True)) * slope
+        else:
+            term = v * g * slope
+            size = term.abs()
+        d = torch.zeros_like(s).scatter_add_(1, at, scale * term)
+        size = torch.zeros_like(s).scatter_add_(1, at, size) * (rel + k * ref.U)
+    tol = abs(scale) * size + ref.TINY
+    if add is not None:
+        d = d + add
+        tol += (add.abs() + d.abs()) * ref.U
+    return d, tol
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T,E,k", [(4096 * 128 + 5003, 8, 2), (4096 * 16 + 4099, 64, 8), (4096 * 4 + 1001, 256, 8),
+                                   (2 * 4096 * 4 + 3, 33, 4), (4096 * 4 + 517, 320, 6)])
+def test_gradient_of_more_tokens_than_workgroups(T, E, k, renormalize, score):
+    """4096 workgroups take what there is in turns: every token against the plain form, some ids out of range."""
+    _announce(f"gradient of many tokens T={T} E={E} k={k} {score} {renormalize}")
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    x = torch.randn((T, E), generator=g, device="cuda")
+    idx = torch.topk(torch.rand((T, E), generator=g, device="cuda"), k, dim=1)[1].to(torch.int32)
+    spoil = torch.rand((T, k), generator=g, device="cuda") < 0.02
+    idx = torch.where(spoil, torch.where(idx % 2 == 0, -1, E + 7), idx).to(torch.int32)
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    for add in (None, torch.randn((T, E), generator=g, device="cuda")):
+        got = moe.moe_route_scored_grad(x, idx, dw, score=score, renormalize=renormalize, scale=2.5, add=add)
+        want, tol = plain_grad(x, idx, dw, add, score, renormalize, 2.5)
+        bad = ~((got.double() - want).abs() <= tol)
+        assert not bad.any(), (bad.sum().item(), bad.nonzero()[0].tolist(), got[bad][0].item(), want[bad][0].item())
