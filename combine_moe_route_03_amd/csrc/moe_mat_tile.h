@@ -991,6 +991,12 @@ inline moe_status_t launch_shape(int shape, const MatArgs& p, hipStream_t stream
     }
 }
 
+// Weights of an expert that a product takes.
+inline bool fits(int64_t n_w, int32_t K)
+{
+    return K % 8 == 0 && n_w <= MOE_MAT_MAX_SIZE && K <= MOE_MAT_MAX_SIZE && n_w * K * 2 < (int64_t)1 << 32;
+}
+
 // The limits that all three products share.
 inline moe_status_t check_sizes(int32_t a_rows, const int32_t* row_token, const int32_t* offsets, int32_t R,
                          int32_t E, int32_t N, int64_t n_w, int32_t K, int32_t act)
@@ -998,8 +1004,8 @@ inline moe_status_t check_sizes(int32_t a_rows, const int32_t* row_token, const 
     if (R < 0 || a_rows < 0 || E < 1 || N < 1 || K < 1 || act < MOE_MAT_NONE || act > MOE_MAT_GELU ||
         (!offsets && E != 1) || (!row_token && R > a_rows) || (row_token && R > 0 && a_rows < 1))
         return MOE_ERR_INVALID;
-    if (K % 8 != 0 || E > MOE_MAX_EXPERTS || n_w > MOE_MAT_MAX_SIZE || K > MOE_MAT_MAX_SIZE ||
-        n_w * K * 2 >= ((int64_t)1 << 32) || (row_token && (int64_t)a_rows * K * 2 >= ((int64_t)1 << 32)))
+    if (E > MOE_MAX_EXPERTS || !fits(n_w, K) ||
+        (row_token && (int64_t)a_rows * K * 2 >= ((int64_t)1 << 32)))
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }

@@ -240,8 +240,8 @@ extern "C" {
 
 size_t moe_expert_matmul_workspace_bytes(int32_t R, int32_t E, int32_t channels, int32_t K)
 {
-    if (R < 1 || E < 1 || channels < 1 || K < 1 || E > MOE_MAX_EXPERTS || channels > MOE_MAT_MAX_SIZE ||
-        K > MOE_MAT_MAX_SIZE || few(R, E, channels))
+    if (R < 1 || E < 1 || channels < 1 || K < 1 || E > MOE_MAX_EXPERTS || !fits(channels, K) ||
+        few(R, E, channels))
         return 0;
     return (size_t)choose<kForward>(R, E, 0, channels, K).part_bytes;
 }
