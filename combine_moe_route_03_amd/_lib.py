@@ -691,28 +691,45 @@ def moe_bias_update(bias: torch.Tensor, expert_counts: torch.Tensor, rate: float
     return out
 
 
+def _wanted(want, names) -> tuple:
+    """What a call is to compute: one of the names, or several of them."""
+    want = (want,) if isinstance(want, str) else tuple(want)
+    if not want or len(set(want)) != len(want) or not set(want) <= set(names):
+        raise ValueError(f"want: {want!r}, needs some of {', '.join(map(repr, names))}, each once")
+    return want
+
+
 def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], token_row: torch.Tensor,
                      topk_w: torch.Tensor, dy: Optional[torch.Tensor] = None,
-                     dtopk_w: Optional[torch.Tensor] = None, stream=None):
-    """Gradient of moe_combine from dout [T,H]: (dy [T*k,H], dtopk_w [T,k]). Without y only dy is
-    computed (in dy's type, bf16 if it is not given) and dtopk_w is None."""
+                     dtopk_w: Optional[torch.Tensor] = None, want=None, stream=None):
+    """Gradient of moe_combine from dout [T,H]: (dy [T*k,H], dtopk_w [T,k]). `want` names those to
+    compute, "dy" or "dtopk_w"; the other is None. By default both, or without y only dy (in its own
+    type, bf16 if it is not given)."""
     dev, T, H = _matrix("dout", dout)
     k = topk_w.shape[-1]
     if k > _MOST or T * k > _MOST:
         _too_large("topk_w", k, T * k)
+    with_dy, with_dw = True, y is not None
+    if want is not None:
+        want = _wanted(want, ("dy", "dtopk_w"))
+        with_dy, with_dw = "dy" in want, "dtopk_w" in want
+    if y is None and (with_dw or dtopk_w is not None):
+        raise ValueError("dtopk_w: needs y")
     wide = y if y is not None else dy
     y_dtype = torch.bfloat16 if wide is None else wide.dtype
     if dy is None:
-        dy = _empty((T * k, H), y_dtype, dev, stream)
-    if y is not None and dtopk_w is None:
-        dtopk_w = _empty((T, k), torch.float32, dev, stream)
-    if y is None and dtopk_w is not None:
-        raise ValueError("dtopk_w: needs y")
+        dy = _empty((T * k, H), y_dtype, dev, stream) if with_dy else None
+    elif not with_dy:
+        raise ValueError("dy: given, and not in want")
+    if dtopk_w is None:
+        dtopk_w = _empty((T, k), torch.float32, dev, stream) if with_dw else None
+    elif not with_dw:
+        raise ValueError("dtopk_w: given, and not in want")
     _enqueue("moe_combine_grad", dev, stream, _arg("dout", dout, _WIDE, (T, H), dev),
-             _dtype_code(dout), _opt("y", y, _WIDE, (T * k, H), dev), _dtype_code(dy),
+             _dtype_code(dout), _opt("y", y, _WIDE, (T * k, H), dev), _dtype_code(y if dy is None else dy),
              _arg("token_row", token_row, torch.int32, (T * k,), dev),
              _arg("topk_w", topk_w, torch.float32, (T, k), dev), T, H, k,
-             _arg("dy", dy, y_dtype, (T * k, H), dev),
+             _opt("dy", dy, y_dtype, (T * k, H), dev),
              _opt("dtopk_w", dtopk_w, torch.float32, (T, k), dev))
     return dy, dtopk_w
 
@@ -811,9 +828,7 @@ def moe_expert_matmul_grad(dy: torch.Tensor, a: Optional[torch.Tensor], w: torch
     row_token is not given. Without a workspace one is allocated for the call."""
     dev, R, N = _matrix("dy", dy)
     E, _, K = _product_sizes(w, act, R)
-    want = (want,) if isinstance(want, str) else tuple(want)
-    if not want or len(set(want)) != len(want) or not set(want) <= {"da", "dw", "dbias"}:
-        raise ValueError(f"want: {want!r}, needs some of 'da', 'dw', 'dbias', each once")
+    want = _wanted(want, ("da", "dw", "dbias"))
     if a is None and ("dw" in want or row_token is not None):
         raise ValueError("a: needed for 'dw', and with row_token")
     A = R if a is None else _matrix("a", a)[1]

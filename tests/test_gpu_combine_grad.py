@@ -78,3 +78,26 @@ def test_combine_grad_past_the_caches(T, k, H, y_dtype, o_dtype):
     """y and dy of more than 256 MB."""
     _announce(f"combine_grad of more than the caches hold T={T} k={k} H={H} {y_dtype} {o_dtype}")
     check(T, k, H, y_dtype, o_dtype)
+
+
+@pytest.mark.parametrize("y_dtype", [BF16, F32])
+@pytest.mark.parametrize("T,k,H", [(5, 3, 264), (1100, 8, 520), (600, 5, 1032), (300, 8, 2056)])
+def test_combine_grad_of_one_kind(T, k, H, y_dtype):
+    """Each gradient alone has the bits that both have; nothing else is needed, and nothing else made."""
+    _announce(f"combine_grad, one of two T={T} k={k} H={H} {y_dtype}")
+    d, y, row, w, dy, dw = check(T, k, H, y_dtype, BF16)
+    none, only = moe.moe_combine_grad(d, y, row, w, want="dtopk_w")
+    assert none is None and torch.equal(only, dw)
+    kept = torch.full_like(dw, 5.0)
+    assert moe.moe_combine_grad(d, y, row, w, want=("dtopk_w",), dtopk_w=kept)[1] is kept and torch.equal(kept, dw)
+    again = torch.full_like(dy, 77.0)
+    only, none = moe.moe_combine_grad(d, y, row, w, want="dy", dy=again)
+    assert none is None and only is again and torch.equal(again, dy)
+    both = moe.moe_combine_grad(d, y, row, w, want=("dtopk_w", "dy"), dy=again.fill_(77.0))
+    assert torch.equal(both[0], dy) and torch.equal(both[1], dw)
+    for bad, error in ((dict(want=()), ValueError), (dict(want="dx"), ValueError), (dict(want=("dy", "dy")), ValueError),
+                       (dict(want="dtopk_w", dy=again), ValueError), (dict(want="dy", dtopk_w=kept), ValueError)):
+        with pytest.raises(error, match="want|dy|dtopk_w"):
+            moe.moe_combine_grad(d, y, row, w, **bad)
+    with pytest.raises(ValueError, match="y"):
+        moe.moe_combine_grad(d, None, row, w, want="dtopk_w")
