@@ -121,3 +121,21 @@ def test_activation_slopes_over_the_whole_range(R, E, N, K, act, dtype):
                     want = d * ref.act(v, "silu")
                 close(f64(da[:, K + c]), want, (20 + 8 * np.minimum(np.abs(v), 100)) * ref.U + ref.half(dtype == BF16),
                       FLUSHED * max(1.0, abs(d)), f"up, column {c}", v)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("R,E,N,K", [(5, 1, 16, 24), (300, 3, 40, 136), (2000, 2, 264, 72), (100, 1, 4096, 64)])
+def test_gradients_through_a_pre_off_16_bytes(R, E, N, K, act):
+    """pre and dbias that begin between 16-byte borders, with plain products among them: the bits of aligned ones."""
+    _announce(f"gradient of {act}, pre off 16 bytes R={R} E={E} N={N} K={K}")
+    g = torch.Generator().manual_seed(R + K)
+    n = R * (2 * K if act == "swiglu" else K)
+    pre = torch.randn(n + 8, generator=g).to(BF16).cuda()
+    dy, a = torch.randn((R, N), generator=g).to(BF16).cuda(), torch.randn((R, K), generator=g).to(BF16).cuda()
+    w = torch.randn((E, N, K), generator=g).to(BF16).cuda()
+    off = None if E == 1 else dev(np.linspace(0, R, E + 1).astype(np.int32))
+    want = ("da", "dw", "dbias")
+    even = moe.moe_expert_matmul_grad(dy, a, w, off, want=want, act=act, pre=pre[1:n + 1].clone().view(R, -1))
+    odd = moe.moe_expert_matmul_grad(dy, a, w, off, want=want, act=act, pre=pre[1:n + 1].view(R, -1),
+                                     dbias=torch.empty(E * N + 4, device="cuda")[1:E * N + 1].view(E, N))
+    assert all(torch.equal(u, v) for u, v in zip(even, odd))
