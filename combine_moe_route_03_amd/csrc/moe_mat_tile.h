@@ -152,7 +152,10 @@ struct Work {
     int32_t first, count;      // weights: the expert's rows
 };
 
-// The steps of part `split` of a sum of `steps`, which may be fewer than the parts.
+// The steps of part `split` of a sum of `steps`. Weights: of an expert's rows, which may be none, or fewer
+// steps than parts; a part without steps gets one behind the end, whose rows are not there. The other sums are
+// as long for every tile, and choose() gives each part four steps at least: there a step behind the end would
+// read the next rows.
 __device__ __forceinline__ void part_of(const MatArgs& p, int32_t split, int32_t steps, Work* w)
 {
     w->split = split;

@@ -175,14 +175,13 @@ __global__ __launch_bounds__(256) void k_join_forward(MatArgs p, const float* __
     }
 }
 
+// At most 2 * 8 of its workgroups for each of less than 256 tiles of few().
 template <bool SWIGLU, typename OUT>
 moe_status_t launch_few(MatArgs p, hipStream_t stream)
 {
     constexpr int kWaves = 8;
     p.n_blocks = (int32_t)div_up(p.N, 16);
     const int64_t blocks = most_tiles(p, 16) * p.n_blocks;
-    if (blocks * 64 * kWaves > INT32_MAX)
-        return MOE_ERR_UNSUPPORTED;
     k_mat_few<kWaves, SWIGLU ? 4 : 2, SWIGLU, OUT><<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p);
     return launched();
 }
