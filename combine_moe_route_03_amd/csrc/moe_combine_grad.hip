@@ -82,9 +82,9 @@ struct CombineGradArgs {
 
 // WAVES wavefronts take a token, or `share` of its slots; a lane holds up to NV pieces of 8 elements of
 // dout, rows longer than that are taken in turns. The slots' products are joined over the wavefronts at
-// the end, in order. 4096 tokens, k = 8, 7168 bf16: 202 us (4.9 TB/s, half of it written) with 8
-// wavefronts of two pieces, 217 with 4 of four, 320 with 2 of seven; two slots' rows on their way at a
-// time 204.
+// the end, in order. 4096 tokens, k = 8, 7168 bf16: 175 to 202 us (5.7 to 4.9 TB/s, half of it written) with
+// 8 wavefronts of two pieces, 217 with 4 of four, 320 with 2 of seven; two slots' rows on their way at a
+// time 204. fp32 rows 405 us (4.9 TB/s), 128 tokens 16.
 template <typename YT, typename OT, int WAVES, int NV, bool NT>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_combine_grad(CombineGradArgs a)
 {
@@ -184,6 +184,10 @@ void launch_combine_grad(CombineGradArgs a, hipStream_t stream)
         k_combine_grad<YT, OT, WAVES, NV, false><<<blocks, kThreads, 0, stream>>>(a);
 }
 
+// One wavefront of two pieces, four of one and eight of two for 4096 tokens, k = 8, in us: bf16 H = 256 8.5, 13.5
+// and 25; 1024 30, 31 and 48; 1032 29, 25 and 31; 2048 79, 56 and 60; 2056 80, 70 and 64; 7168 190, 186 and 188.
+// fp32 H = 256 16, 21 and 36; 520 27, 25 and 30; 1024 64, 62 and 62; 1032 78, 70 and 69; 2048 122, 126 and 121;
+// 2056 158, 146 and 136; 7168 433, 454 and 438. Of 128 tokens by 7168 14, 8.7 and 8.2 (bf16).
 template <typename YT, typename OT>
 void launch_combine_grad(const CombineGradArgs& a, hipStream_t stream)
 {

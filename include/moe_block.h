@@ -94,6 +94,8 @@ moe_status_t moe_bias_update(const float* bias, const int32_t* expert_counts, in
  *   dout [T, H] dout_dtype, y and dy [T * k, H] y_dtype: MOE_F32 or MOE_BF16 each, 16-byte aligned.
  *   dy or dtopk_w may be NULL (not both): what it would hold is not computed, y and topk_w are not
  *   read for it and may be NULL then. Rows outside [0, T * k) are skipped: dtopk_w is 0 there.
+ *   token_row is that of moe_dispatch_layout. Where several slots name one row, an element of dy is that
+ *   of any one of them, not their sum.
  * Requires H % 8 == 0 (else MOE_ERR_UNSUPPORTED). Rows that no slot names are left as they were.
  */
 moe_status_t moe_combine_grad(const void* dout, moe_dtype_t dout_dtype, const void* y,
