@@ -701,7 +701,7 @@ def _wanted(want, names) -> tuple:
 
 def moe_combine_grad(dout: torch.Tensor, y: Optional[torch.Tensor], token_row: torch.Tensor,
                      topk_w: torch.Tensor, dy: Optional[torch.Tensor] = None,
-                     dtopk_w: Optional[torch.Tensor] = None, want=None, stream=None):
+                     dtopk_w: Optional[torch.Tensor] = None, stream=None, want=None):
     """Gradient of moe_combine from dout [T,H]: (dy [T*k,H], dtopk_w [T,k]). `want` names those to
     compute, "dy" or "dtopk_w"; the other is None. By default both, or without y only dy (in its own
     type, bf16 if it is not given)."""

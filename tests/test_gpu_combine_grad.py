@@ -101,3 +101,17 @@ def test_combine_grad_of_one_kind(T, k, H, y_dtype):
             moe.moe_combine_grad(d, y, row, w, **bad)
     with pytest.raises(ValueError, match="y"):
         moe.moe_combine_grad(d, None, row, w, want="dtopk_w")
+
+
+def test_combine_grad_arguments_by_place():
+    """dy, dtopk_w and the stream by their places."""
+    _announce("combine_grad, arguments by place")
+    d, y, row, w = made(40, 4, 264, BF16, BF16)
+    row = torch.where(row < 0, -1, row)
+    want = moe.moe_combine_grad(d, y, row, w, dy=torch.zeros_like(y))
+    dy, dw = torch.zeros_like(y), torch.empty_like(w)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    got = moe.moe_combine_grad(d, y, row, w, dy, dw, stream)
+    stream.synchronize()
+    assert got[0] is dy and got[1] is dw and torch.equal(dy, want[0]) and torch.equal(dw, want[1])
