@@ -84,7 +84,7 @@ struct CombineGradArgs {
 // dout, rows longer than that are taken in turns. The slots' products are joined over the wavefronts at
 // the end, in order. 4096 tokens, k = 8, 7168 bf16: 175 to 202 us (5.7 to 4.9 TB/s, half of it written) with
 // 8 wavefronts of two pieces, 217 with 4 of four, 320 with 2 of seven; two slots' rows on their way at a
-// time 204. fp32 rows 405 us (4.9 TB/s), 128 tokens 16.
+// time 204. fp32 rows 405 to 446 us (4.9 to 4.5 TB/s), 128 tokens 16.
 template <typename YT, typename OT, int WAVES, int NV, bool NT>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_combine_grad(CombineGradArgs a)
 {

@@ -421,7 +421,7 @@ __device__ __forceinline__ float sigmoid_of(float x)
 // sure of it (p 1 - 1e-6: 1e-6 q), so q counts from that expert's, which leaves the others' part of the sum:
 // with c the q of the p over 1/2, if there is one, it is (q_e - c) - sum_i p_i (q_i - c). Logits are read once
 // and the gradient is written once, with p made again from them in fp32: 65536 tokens of 256 experts, 8
-// chosen, 21.4 us, 6.5 TB/s, HBM's rate.
+// chosen, 21.2 to 22.2 us, 6.5 to 6.2 TB/s, HBM's rate.
 template <int G, int NV, int VEC>
 __global__ __launch_bounds__(256) void k_scored_grad_all(ScoredGradArgs a)
 {
@@ -474,11 +474,11 @@ __global__ __launch_bounds__(256) void k_scored_grad_all(ScoredGradArgs a)
 // The other weights: only the chosen logits take part. With S the sum of the chosen scores and v_j =
 // s_j / S, dl_j = scale v_j (dw_j - sum_i v_i dw_i), times 1 - s_j for the sigmoid; without the sum,
 // dl_j = scale s_j (1 - s_j) dw_j. Scores go into the quotients relative to that of the largest
-// chosen logit (for the sigmoid where that is negative), so that none of them vanishes, and dw counts from
-// that of the v over 1/2, if there is one, so that no difference loses what a sure token leaves of it. G lanes take a
-// token, lane j the slots j, j + G, ...; the terms are added to the row in LDS of the group's own, which is
-// written whole, zeros and all. Its writes and a chain of two loads (ids, then their logits) bound it: 4096
-// tokens of 384 experts with a gradient to add 4.3 us, 2.9 TB/s, most of it in the Infinity Cache.
+// chosen logit (for the sigmoid where that is negative), so that none of them vanishes, and dw counts
+// from that of the v over 1/2, if there is one, as above. G lanes take a token, lane j the slots j, j + G,
+// ...; the terms are added to the row in LDS of the group's own, which is written whole, zeros and all. Its
+// writes and a chain of two loads (ids, then their logits) bound it: 4096 tokens of 384 experts with a
+// gradient to add 4.4 us, 2.9 TB/s, most of it in the Infinity Cache.
 template <int G, int NV, int VEC, bool SIGMOID, bool RENORM>
 __global__ __launch_bounds__(256) void k_scored_grad(ScoredGradArgs a)
 {

@@ -340,10 +340,10 @@ __device__ __forceinline__ bf16x8 read_across(const int8_t* p)
 // that take no part and channels beyond the last cost no instructions. Sums stay in fp32 from the first
 // product to the epilogue; pre, out and da are rounded to their type once, at the end.
 // Bound by LDS and the matrix cores together: a 256 x 256 step takes 1.71 us, its products alone 0.86 at
-// 2.5 PFLOP/s. 8192 x 8192 x 8192 in forward form 926 us when taken apart (860 to
-// 890 since), without the loads 770, without the LDS reads 784, without the products 516: each takes over
+// 2.5 PFLOP/s. 8192 x 8192 x 8192 in forward form 926 us when taken apart (868 to
+// 912 since), without the loads 770, without the LDS reads 784, without the products 516: each takes over
 // half of the time and they overlap as far as two stages of 64 KB allow (a third does not fit). The
-// gradients of 8192^3: rows 880, weights 910 to 940 (a library product 779).
+// gradients of 8192^3: rows 870 to 910, weights 905 to 970 (a library product 779).
 // FULL: with pre, a residual, or an activation other than SwiGLU (rows: with an activation's
 // gradient), whose registers the other calls do not have to give up.
 template <int MODE, int BM, int BN, int WM, int WN, int STAGES, bool SWIGLU, bool FULL,

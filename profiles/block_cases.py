@@ -21,6 +21,17 @@ def more(ops):
         ops._product("gate, 64 tokens", 64, 1, 1, 384, 7168, *plain),
         ops._product("gate, 4096 tokens", 4096, 1, 1, 384, 7168, *plain),
         ops._product("8 rows of 8 experts", 1, 8, 128, 1024, 2048, "swiglu", True, "bf16", 0.0, False, False, False),
+        *(ops._product(f"4096 cubed, {act}{', residual' if res else ''}{', pre' if pre else ''}", 4096, 1, 1, 4096, 4096,
+                       act, False, dtype, 0.0, True, res, pre)
+          for act, dtype, res, pre in (("none", "bf16", False, False), ("none", "bf16", True, False),
+                                       ("none", "f32", True, False), ("relu", "bf16", False, False),
+                                       ("silu", "bf16", False, False), ("gelu", "bf16", False, False),
+                                       ("gelu", "bf16", True, True))),
+        *(ops._back(f"back 4096 cubed, {act}", 4096, 1, 1, 4096, 4096, act, False, "bf16", "f32", 0.0, False)
+          for act in ("none", "relu", "gelu", "swiglu")),
+        ops._combine("combine back, fp32", 4096, 8, 7168, "f32", "f32"),
+        ops._combine("combine back, fp32 rows", 4096, 8, 7168, "f32", "bf16"),
+        ops._combine("combine back, fp32 of 128 tokens", 128, 8, 7168, "f32", "f32"),
     ]
 
 
